@@ -318,6 +318,116 @@ int moe_route(const moe_dims *dims, const uint16_t *x, const float *router_w,
               int32_t *inv, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * Operators beside the forward: a bf16 expert layer's products one by one,
+ * with their gradients, for programs that train the layer or put dense layers
+ * of their own next to it. They follow the conventions above; all data is bf16
+ * unless stated, row-major and 16-byte aligned, with feature widths (N, K, h,
+ * d) that are multiples of 8 in [8, 2^20] and row counts in [0, 2^30]. Products
+ * and sums are accumulated in fp32 and rounded once, to the output's type, at
+ * the end; reduction orders are fixed, so a call on the same inputs gives the
+ * same bits. Outputs must not overlap inputs or each other, except where an
+ * entry point says that they may be the same buffer (MOE_ERR_INVALID_ARG). NaN
+ * and infinities in the inputs propagate as in the formulas, to the outputs
+ * whose formula reads them.
+ *
+ * Except for moe_linear_dz's column sums none needs a workspace, so calls on
+ * different streams, and captured graphs of them, share no memory.
+ */
+
+/* Activations of moe_linear / moe_linear_dz. */
+enum moe_act {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,
+    MOE_ACT_SILU = 2,      /* z sigmoid(z) */
+    MOE_ACT_GELU = 3,      /* z Phi(z), by erf */
+    MOE_ACT_GELU_TANH = 4  /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+};
+
+/*
+ * Products grouped by expert. Rows offsets[e] .. offsets[e+1] - 1 of the row
+ * matrices belong to group e (the `offsets` of moe_route; int32 [E+1] on the
+ * device, ascending, within [0, P]); E in [1, MOE_MAX_EXPERTS]; E*N*K at most 2^39.
+ * A NULL `offsets` with E = 1 means one group of all P rows (a dense layer).
+ *   moe_grouped_matmul:     y[s]  = x[s] W_e^T           x [P, K], w [E, N, K], y [P, N]
+ *   moe_grouped_matmul_dx:  dx[s] = dy[s] W_e            dy [P, N], dx [P, K]
+ *   moe_grouped_matmul_dw:  dw_e  = sum over the rows s of e of dy[s]^T x[s]
+ *                                                        dw [E, N, K]; added to the
+ *                           values in dw with `accumulate` (one rounding of the sum)
+ * The output is bf16, or fp32 with out_fp32. Groups may be empty: their dw is
+ * zero (or unchanged with accumulate). Rows outside every group are not read,
+ * and their rows of y and dx are left as they were. Offsets outside [0, P] are
+ * clamped to it and a descending pair is an empty group.
+ */
+int moe_grouped_matmul(const uint16_t *x, const uint16_t *w, const int32_t *offsets,
+                       int64_t P, int64_t E, int64_t N, int64_t K, void *y,
+                       int32_t out_fp32, void *stream);
+int moe_grouped_matmul_dx(const uint16_t *dy, const uint16_t *w, const int32_t *offsets,
+                          int64_t P, int64_t E, int64_t N, int64_t K, void *dx,
+                          int32_t out_fp32, void *stream);
+int moe_grouped_matmul_dw(const uint16_t *dy, const uint16_t *x, const int32_t *offsets,
+                          int64_t P, int64_t E, int64_t N, int64_t K, void *dw,
+                          int32_t out_fp32, int32_t accumulate, void *stream);
+
+/*
+ * Dense layer y = act(x W^T + bias) + residual, one pass: x [T, K], w [N, K],
+ * bias fp32 [N] or NULL, residual [T, N] or NULL, y [T, N] bf16 or fp32. With z
+ * non-NULL it also writes z = x W^T + bias [T, N] (rounded to bf16; y is computed
+ * from the unrounded sum), which moe_linear_dz reads. A bf16 y may be the same
+ * buffer as residual.
+ */
+int moe_linear(const uint16_t *x, const uint16_t *w, const float *bias, int32_t act,
+               const uint16_t *residual, int64_t T, int64_t N, int64_t K, void *y,
+               int32_t out_fp32, uint16_t *z, void *stream);
+
+/*
+ * The gradient of moe_linear through its activation: dz = dy * act'(z) [T, N] and
+ * db = the column sums of dz before its rounding, fp32 [N] (NULL: not wanted).
+ * relu'(0) = 0. The gradients of x and W are then moe_grouped_matmul_dx /
+ * _dw of dz with one group; that of the residual is dy. With act none dz is dy:
+ * dz must be NULL, z is not read, and db must be wanted. dz may be the same
+ * buffer as dy or z. T = 0 gives db = 0. The workspace (at least
+ * moe_linear_dz_workspace_bytes, 256-byte aligned) is needed for db alone.
+ */
+size_t moe_linear_dz_workspace_bytes(int64_t T, int64_t N);
+int moe_linear_dz(const uint16_t *dy, const uint16_t *z, int32_t act, int64_t T, int64_t N,
+                  uint16_t *dz, float *db, void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+/*
+ * SwiGLU of rows that hold both up-projections side by side, z = [g | u] [rows, 2h]:
+ * y = silu(g) * u [rows, h]; and its gradient dz = [dy u silu'(g) | dy silu(g)]
+ * [rows, 2h], which may be the same buffer as z.
+ */
+int moe_swiglu(const uint16_t *z, int64_t rows, int64_t h, uint16_t *y, void *stream);
+int moe_swiglu_backward(const uint16_t *dy, const uint16_t *z, int64_t rows, int64_t h,
+                        uint16_t *dz, void *stream);
+
+/*
+ * Rows moved between tokens and their experts, by the `perm` and `inv` of
+ * moe_route (int32 [T*top_k]; pair = t*top_k + j; top_k in [1, MOE_MAX_TOP_K]).
+ *   moe_permute_rows:  xp[s] = x[perm[s] / top_k]        x [T, d], xp [T*top_k, d]
+ *   moe_combine:       y[t] = sum_j gates[t, j] o[inv[t, j]] + residual[t]
+ *                      o [T*top_k, d] bf16, or fp32 with o_fp32; gates fp32 [T, top_k],
+ *                      NULL for 1; residual [T, d] or NULL; y [T, d], which may be the
+ *                      same buffer as residual. Without gates it is the gradient of
+ *                      moe_permute_rows.
+ *   moe_combine_backward:  d_o[inv[t, j]] = gates[t, j] dy[t]      [T*top_k, d] bf16
+ *                      d_gates[t, j] = <dy[t], o[inv[t, j]]>        fp32, NULL: not wanted
+ *                      (then o is not read)
+ * The gradient of residual is dy. An entry of perm or inv outside [0, T*top_k)
+ * stands for a row of zeros (its d_gates is 0, and nothing of d_o is written for it).
+ */
+int moe_permute_rows(const uint16_t *x, const int32_t *perm, int64_t T, int32_t top_k,
+                     int64_t d, uint16_t *xp, void *stream);
+int moe_combine(const void *o, int32_t o_fp32, const int32_t *inv, const float *gates,
+                const uint16_t *residual, int64_t T, int32_t top_k, int64_t d, uint16_t *y,
+                void *stream);
+int moe_combine_backward(const uint16_t *dy, const void *o, int32_t o_fp32,
+                         const int32_t *inv, const float *gates, int64_t T, int32_t top_k,
+                         int64_t d, uint16_t *d_o, float *d_gates, void *stream);
+
+/*
  * Per-stage timing for benchmarks (not part of the layer's arithmetic).
  * While enabled, each stage of every moe_forward / moe_route call (and each
  * int4 quantizer call, as MOE_STAGE_QUANTIZE) is timed by

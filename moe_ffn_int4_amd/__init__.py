@@ -124,6 +124,29 @@ def lib() -> ctypes.CDLL:
         L.moe_route_workspace_bytes.restype = sz
         L.moe_route.argtypes = [ctypes.POINTER(_Dims), P, P, P, P, P, P, P, P, P, P, P, sz, P]
         L.moe_route.restype = ctypes.c_int
+        products = [P, P, P, i64, i64, i64, i64, P, i32]
+        L.moe_grouped_matmul.argtypes = products + [P]
+        L.moe_grouped_matmul.restype = ctypes.c_int
+        L.moe_grouped_matmul_dx.argtypes = products + [P]
+        L.moe_grouped_matmul_dx.restype = ctypes.c_int
+        L.moe_grouped_matmul_dw.argtypes = products + [i32, P]
+        L.moe_grouped_matmul_dw.restype = ctypes.c_int
+        L.moe_linear.argtypes = [P, P, P, i32, P, i64, i64, i64, P, i32, P, P]
+        L.moe_linear.restype = ctypes.c_int
+        L.moe_linear_dz_workspace_bytes.argtypes = [i64, i64]
+        L.moe_linear_dz_workspace_bytes.restype = sz
+        L.moe_linear_dz.argtypes = [P, P, i32, i64, i64, P, P, P, sz, P]
+        L.moe_linear_dz.restype = ctypes.c_int
+        L.moe_swiglu.argtypes = [P, i64, i64, P, P]
+        L.moe_swiglu.restype = ctypes.c_int
+        L.moe_swiglu_backward.argtypes = [P, P, i64, i64, P, P]
+        L.moe_swiglu_backward.restype = ctypes.c_int
+        L.moe_permute_rows.argtypes = [P, P, i64, i32, i64, P, P]
+        L.moe_permute_rows.restype = ctypes.c_int
+        L.moe_combine.argtypes = [P, i32, P, P, P, i64, i32, i64, P, P]
+        L.moe_combine.restype = ctypes.c_int
+        L.moe_combine_backward.argtypes = [P, P, i32, P, P, i64, i32, i64, P, P, P]
+        L.moe_combine_backward.restype = ctypes.c_int
         L.moe_profile_enable.argtypes = [ctypes.c_int]
         L.moe_profile_enable.restype = ctypes.c_int
         L.moe_profile_read.argtypes = [P, P, ctypes.c_int]
@@ -568,6 +591,321 @@ def route(x: torch.Tensor, router_w: torch.Tensor, router_b: Optional[torch.Tens
         _ptr(out["gates"]), _ptr(out["logits"]), _ptr(out["counts"]), _ptr(out["offsets"]),
         _ptr(out["perm"]), _ptr(out["inv"]), _ptr(workspace), workspace.numel(), _stream(dev)))
     return out
+
+
+# ------------------------------------- operators for training and dense layers
+#
+# The layer's products one by one, with their gradients. They run on the current
+# stream of their first argument's device, which need not be the current device; all
+# tensors must be on it.
+
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+_OUT = (torch.bfloat16, torch.float32)
+
+
+def _run(fn, first: torch.Tensor, *args) -> None:
+    """fn(*args, stream) with `first`'s device current."""
+    dev = first.device
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _same_device(first: torch.Tensor, *rest: Optional[torch.Tensor]) -> None:
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device is wanted")
+
+
+def _output(out: Optional[torch.Tensor], name: str, shape, dtype, first: torch.Tensor) -> torch.Tensor:
+    if dtype not in _OUT:
+        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=first.device)
+    _need(out, name, dtype, shape)
+    _same_device(first, out)
+    return out
+
+
+def _two_dim(t: torch.Tensor, name: str) -> None:
+    _need(t, name, torch.bfloat16)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+
+
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act {act!r} unknown: one of {', '.join(ACTS)}")
+    return ACTS[act]
+
+
+def _groups(w: torch.Tensor, offsets: torch.Tensor, first: torch.Tensor):
+    _need(w, "w", torch.bfloat16)
+    if w.dim() != 3:
+        raise ValueError("w must be [E, N, K]")
+    _need(offsets, "offsets", torch.int32, (w.shape[0] + 1,))
+    _same_device(first, w, offsets)
+    return w.shape
+
+
+def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+                   out: Optional[torch.Tensor] = None,
+                   out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Products of the rows of each expert with its weights: y[s] = x[s] w[e]^T for
+    rows s in [offsets[e], offsets[e+1]).
+
+    x bf16 [P, K] (rows in expert order, ``permute_rows``), w bf16 [E, N, K] row-major,
+    offsets int32 [E+1] (``route``), y [P, N] bf16 or fp32. N and K multiples of 8.
+    Experts may have no rows; rows of ``out`` outside every expert stay as they were."""
+    _two_dim(x, "x")
+    E, N, K = _groups(w, offsets, x)
+    P = x.shape[0]
+    if x.shape[1] != K:
+        raise ValueError(f"x has {x.shape[1]} columns, w {K}")
+    y = _output(out, "out", (P, N), out.dtype if out is not None else out_dtype, x)
+    _run(lib().moe_grouped_matmul, x, x.data_ptr(), w.data_ptr(), offsets.data_ptr(), P, E, N, K,
+         y.data_ptr(), y.dtype == torch.float32)
+    return y
+
+
+def grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+                      out: Optional[torch.Tensor] = None,
+                      out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Gradient of ``grouped_matmul`` for its rows: dx[s] = dy[s] w[e]; dy bf16 [P, N],
+    dx [P, K] bf16 or fp32."""
+    _two_dim(dy, "dy")
+    E, N, K = _groups(w, offsets, dy)
+    P = dy.shape[0]
+    if dy.shape[1] != N:
+        raise ValueError(f"dy has {dy.shape[1]} columns, w {N} rows")
+    dx = _output(out, "out", (P, K), out.dtype if out is not None else out_dtype, dy)
+    _run(lib().moe_grouped_matmul_dx, dy, dy.data_ptr(), w.data_ptr(), offsets.data_ptr(), P, E, N, K,
+         dx.data_ptr(), dx.dtype == torch.float32)
+    return dx
+
+
+def grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
+                      out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                      accumulate: bool = False) -> torch.Tensor:
+    """Gradient of ``grouped_matmul`` for its weights: dw[e] = sum over the expert's
+    rows of dy[s]^T x[s], [E, N, K] bf16 or fp32; zero for an expert without rows.
+    ``accumulate`` adds it to ``out``."""
+    _two_dim(dy, "dy")
+    _two_dim(x, "x")
+    _need(offsets, "offsets", torch.int32)
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must be [E + 1]")
+    _same_device(dy, x, offsets)
+    P, N, K, E = dy.shape[0], dy.shape[1], x.shape[1], offsets.shape[0] - 1
+    if x.shape[0] != P:
+        raise ValueError(f"dy has {P} rows, x {x.shape[0]}")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    dw = _output(out, "out", (E, N, K), out.dtype if out is not None else out_dtype, dy)
+    _run(lib().moe_grouped_matmul_dw, dy, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), P, E, N, K,
+         dw.data_ptr(), dw.dtype == torch.float32, bool(accumulate))
+    return dw
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
+           residual: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+           out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Dense layer act(x w^T + bias) + residual in one pass.
+
+    x bf16 [T, K], w bf16 [N, K] row-major, bias fp32 [N], residual bf16 [T, N], act
+    one of ``ACTS``. ``z`` (bf16 [T, N]), if given, receives x w^T + bias for
+    ``linear_dz``. A bf16 ``out`` may be ``residual`` itself. N and K multiples of 8."""
+    _two_dim(x, "x")
+    _two_dim(w, "w")
+    (T, K), N = x.shape, w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"x has {K} columns, w {w.shape[1]}")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (N,))
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (T, N))
+    if z is not None:
+        _need(z, "z", torch.bfloat16, (T, N))
+    _same_device(x, w, bias, residual, z)
+    y = _output(out, "out", (T, N), out.dtype if out is not None else out_dtype, x)
+    _run(lib().moe_linear, x, x.data_ptr(), w.data_ptr(), _ptr(bias), _act(act), _ptr(residual), T, N, K,
+         y.data_ptr(), y.dtype == torch.float32, _ptr(z))
+    return y
+
+
+def linear_dz_workspace_bytes(T: int, N: int) -> int:
+    """Workspace bytes of ``linear_dz`` for dz [T, N]."""
+    n = lib().moe_linear_dz_workspace_bytes(int(T), int(N))
+    if n == 0:
+        raise ValueError(f"invalid dims T={T} N={N}")
+    return n
+
+
+def linear_dz(dy: torch.Tensor, z: Optional[torch.Tensor], act: str = "none",
+              out: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None):
+    """Gradient of ``linear`` through its activation: (dz, db) with dz = dy * act'(z)
+    bf16 [T, N] and db fp32 [N] the column sums of dz, the bias's gradient. With act
+    "none" dz is dy itself and z is not read. ``out`` may be dy or z."""
+    _two_dim(dy, "dy")
+    T, N = dy.shape
+    code = _act(act)
+    if code:
+        if z is None:
+            raise ValueError(f"act {act!r} needs z")
+        _need(z, "z", torch.bfloat16, (T, N))
+        dz = _output(out, "out", (T, N), torch.bfloat16, dy)
+    else:
+        if out is not None:
+            raise ValueError("act 'none' writes no dz: it is dy")
+        z, dz = None, None
+    if db is None:
+        db = torch.empty(N, dtype=torch.float32, device=dy.device)
+    _need(db, "db", torch.float32, (N,))
+    if workspace is None:
+        workspace = torch.empty(linear_dz_workspace_bytes(T, N), dtype=torch.uint8, device=dy.device)
+    _need(workspace, "workspace", torch.uint8)
+    _same_device(dy, z, db, workspace)
+    _run(lib().moe_linear_dz, dy, dy.data_ptr(), _ptr(z), code, T, N, _ptr(dz), db.data_ptr(),
+         workspace.data_ptr(), workspace.numel())
+    return (dy if dz is None else dz), db
+
+
+def linear_dx(dz: torch.Tensor, w: torch.Tensor, out: Optional[torch.Tensor] = None,
+              out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Gradient of ``linear`` for x: dz w, dz bf16 [T, N], w bf16 [N, K]."""
+    _two_dim(dz, "dz")
+    _two_dim(w, "w")
+    (T, N), K = dz.shape, w.shape[1]
+    if w.shape[0] != N:
+        raise ValueError(f"dz has {N} columns, w {w.shape[0]} rows")
+    _same_device(dz, w)
+    dx = _output(out, "out", (T, K), out.dtype if out is not None else out_dtype, dz)
+    _run(lib().moe_grouped_matmul_dx, dz, dz.data_ptr(), w.data_ptr(), None, T, 1, N, K,
+         dx.data_ptr(), dx.dtype == torch.float32)
+    return dx
+
+
+def linear_dw(dz: torch.Tensor, x: torch.Tensor, out: Optional[torch.Tensor] = None,
+              out_dtype: torch.dtype = torch.bfloat16, accumulate: bool = False) -> torch.Tensor:
+    """Gradient of ``linear`` for w: dz^T x, [N, K]; ``accumulate`` adds it to ``out``."""
+    _two_dim(dz, "dz")
+    _two_dim(x, "x")
+    (T, N), K = dz.shape, x.shape[1]
+    if x.shape[0] != T:
+        raise ValueError(f"dz has {T} rows, x {x.shape[0]}")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    _same_device(dz, x)
+    dw = _output(out, "out", (N, K), out.dtype if out is not None else out_dtype, dz)
+    _run(lib().moe_grouped_matmul_dw, dz, dz.data_ptr(), x.data_ptr(), None, T, 1, N, K,
+         dw.data_ptr(), dw.dtype == torch.float32, bool(accumulate))
+    return dw
+
+
+def swiglu(z: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """silu(g) * u of rows z = [g | u], bf16 [rows, 2h] -> [rows, h] (h a multiple of 8)."""
+    _two_dim(z, "z")
+    rows, h = z.shape[0], z.shape[1] // 2
+    if z.shape[1] != 2 * h:
+        raise ValueError("z must have an even number of columns")
+    y = _output(out, "out", (rows, h), torch.bfloat16, z)
+    _run(lib().moe_swiglu, z, z.data_ptr(), rows, h, y.data_ptr())
+    return y
+
+
+def swiglu_backward(dy: torch.Tensor, z: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of ``swiglu``: dz = [dy u silu'(g) | dy silu(g)], bf16 [rows, 2h].
+    ``out`` may be z."""
+    _two_dim(dy, "dy")
+    rows, h = dy.shape
+    _need(z, "z", torch.bfloat16, (rows, 2 * h))
+    _same_device(dy, z)
+    dz = _output(out, "out", (rows, 2 * h), torch.bfloat16, dy)
+    _run(lib().moe_swiglu_backward, dy, dy.data_ptr(), z.data_ptr(), rows, h, dz.data_ptr())
+    return dz
+
+
+def permute_rows(x: torch.Tensor, perm: torch.Tensor, top_k: int,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Tokens copied to their expert rows: xp[s] = x[perm[s] // top_k]; x bf16 [T, d],
+    perm int32 [T*top_k] (``route``). Its gradient is ``combine`` without gates."""
+    _two_dim(x, "x")
+    T, d = x.shape
+    _need(perm, "perm", torch.int32)
+    if perm.numel() != T * top_k:
+        raise ValueError(f"perm has {perm.numel()} entries, expected {T * top_k}")
+    _same_device(x, perm)
+    xp = _output(out, "out", (T * top_k, d), torch.bfloat16, x)
+    _run(lib().moe_permute_rows, x, x.data_ptr(), perm.data_ptr(), T, top_k, d, xp.data_ptr())
+    return xp
+
+
+def _pairs(T: int, inv: torch.Tensor, gates: Optional[torch.Tensor], top_k: int) -> None:
+    _need(inv, "inv", torch.int32)
+    if inv.numel() != T * top_k:
+        raise ValueError(f"inv has {inv.numel()} entries, expected {T * top_k}")
+    if gates is not None:
+        _need(gates, "gates", torch.float32, (T, top_k))
+
+
+def combine(o: torch.Tensor, inv: torch.Tensor, gates: Optional[torch.Tensor] = None,
+            residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+            top_k: Optional[int] = None) -> torch.Tensor:
+    """Expert rows summed back to their tokens: y[t] = sum_j gates[t, j] o[inv[t, j]] +
+    residual[t], bf16 [T, d].
+
+    o bf16 or fp32 [T*top_k, d], inv int32 [T, top_k] or flat (``route``), gates fp32
+    [T, top_k] (none: 1). top_k comes from gates or a 2-D inv, or is given. ``out`` may
+    be ``residual`` itself."""
+    if not isinstance(o, torch.Tensor) or o.dtype not in _OUT:
+        raise TypeError("o must be a bf16 or fp32 tensor")
+    _need(o, "o", o.dtype)
+    if o.dim() != 2:
+        raise ValueError("o must be 2-D")
+    if top_k is None:
+        if gates is not None:
+            top_k = gates.shape[-1]
+        elif inv.dim() == 2:
+            top_k = inv.shape[1]
+        else:
+            raise ValueError("a flat inv without gates needs top_k")
+    P, d = o.shape
+    if top_k < 1 or P % top_k:
+        raise ValueError(f"o has {P} rows: not a multiple of top_k = {top_k}")
+    T = P // top_k
+    _pairs(T, inv, gates, top_k)
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (T, d))
+    _same_device(o, inv, gates, residual)
+    y = _output(out, "out", (T, d), torch.bfloat16, o)
+    _run(lib().moe_combine, o, o.data_ptr(), o.dtype == torch.float32, inv.data_ptr(), _ptr(gates),
+         _ptr(residual), T, top_k, d, y.data_ptr())
+    return y
+
+
+def combine_backward(dy: torch.Tensor, o: torch.Tensor, inv: torch.Tensor, gates: torch.Tensor,
+                     out: Optional[torch.Tensor] = None):
+    """Gradient of ``combine``: (d_o, d_gates) with d_o[inv[t, j]] = gates[t, j] dy[t], bf16
+    [T*top_k, d], and d_gates[t, j] = <dy[t], o[inv[t, j]]>, fp32 [T, top_k]."""
+    _two_dim(dy, "dy")
+    T, d = dy.shape
+    _need(gates, "gates", torch.float32)
+    if gates.dim() != 2 or gates.shape[0] != T:
+        raise ValueError(f"gates must be [{T}, top_k]")
+    top_k = gates.shape[1]
+    _pairs(T, inv, gates, top_k)
+    if not isinstance(o, torch.Tensor) or o.dtype not in _OUT:
+        raise TypeError("o must be a bf16 or fp32 tensor")
+    _need(o, "o", o.dtype, (T * top_k, d))
+    _same_device(dy, o, inv, gates)
+    d_o = _output(out, "out", (T * top_k, d), torch.bfloat16, dy)
+    d_gates = torch.empty(T, top_k, dtype=torch.float32, device=dy.device)
+    _run(lib().moe_combine_backward, dy, dy.data_ptr(), o.data_ptr(), o.dtype == torch.float32,
+         inv.data_ptr(), gates.data_ptr(), T, top_k, d, d_o.data_ptr(), d_gates.data_ptr())
+    return d_o, d_gates
 
 
 def untile_int4(q: torch.Tensor, rows: int, K: int) -> torch.Tensor:

@@ -14,6 +14,7 @@
 #include <string>
 #include <vector>
 
+#include "host.h"
 #include "kernels.h"
 
 static_assert(MOE_MAX_EXPERTS == moe::kMaxExperts, "expert limit mismatch");
@@ -26,11 +27,10 @@ LaunchTiming& launch_timing() {
 }
 }  // namespace moe
 
-namespace {
+namespace moe {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 int fail(int status, const char* fmt, ...) {
     char buf[512];
     va_list ap;
@@ -41,11 +41,53 @@ int fail(int status, const char* fmt, ...) {
     return status;
 }
 
+void clear_error() { g_last_error.clear(); }
+
 int hip_fail(hipError_t e, const char* what) {
     return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int check_ptr(const void* p, const char* name, size_t align) {
+    if (!p) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!aligned(p, align)) return fail(MOE_ERR_INVALID_ARG, "%s is not %zu-byte aligned", name, align);
+    return MOE_OK;
+}
+
+// Cached "is gfx950" per device ordinal.
+int device_ok() {
+    static std::mutex mu;
+    static int state[64];  // 0 unknown, 1 ok, 2 unsupported
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    if (dev < 0 || dev >= 64) return fail(MOE_ERR_UNSUPPORTED_DEVICE, "device ordinal %d", dev);
+    std::lock_guard<std::mutex> lock(mu);
+    if (state[dev] == 0) {
+        hipDeviceProp_t prop;
+        e = hipGetDeviceProperties(&prop, dev);
+        if (e != hipSuccess) return hip_fail(e, "hipGetDeviceProperties");
+        state[dev] = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
+        if (state[dev] == 2) {
+            return fail(MOE_ERR_UNSUPPORTED_DEVICE, "device %d is %s, this library is built for gfx950",
+                        dev, prop.gcnArchName);
+        }
+    }
+    if (state[dev] == 2) return fail(MOE_ERR_UNSUPPORTED_DEVICE, "device %d is not gfx950", dev);
+    return MOE_OK;
+}
+
+}  // namespace moe
+
+namespace {
+
+using moe::aligned;
+using moe::check_ptr;
+using moe::device_ok;
+using moe::fail;
+using moe::g_last_error;
+using moe::hip_fail;
 
 constexpr size_t kAlign = 256;
 size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
@@ -149,24 +191,6 @@ int check_dims(const moe_dims* d) {
     return MOE_OK;
 }
 
-int check_ptr(const void* p, const char* name, size_t align = 16) {
-    if (!p) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
-    if (!aligned(p, align)) return fail(MOE_ERR_INVALID_ARG, "%s is not %zu-byte aligned", name, align);
-    return MOE_OK;
-}
-
-#define CHECK(expr)                   \
-    do {                              \
-        int rc_ = (expr);             \
-        if (rc_ != MOE_OK) return rc_; \
-    } while (0)
-
-#define HIP_CHECK(expr, what)                    \
-    do {                                         \
-        hipError_t e_ = (expr);                  \
-        if (e_ != hipSuccess) return hip_fail(e_, what); \
-    } while (0)
-
 // ---- optional per-stage timing (moe_profile_*)
 struct Prof {
     std::mutex mu;
@@ -224,29 +248,6 @@ int timed(int stage, hipStream_t s, const char* what, F&& fn) {
     }
     HIP_CHECK(e, what);
     (void)s;
-    return MOE_OK;
-}
-
-// Cached "is gfx950" per device ordinal.
-int device_ok() {
-    static std::mutex mu;
-    static int state[64];  // 0 unknown, 1 ok, 2 unsupported
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
-    if (dev < 0 || dev >= 64) return fail(MOE_ERR_UNSUPPORTED_DEVICE, "device ordinal %d", dev);
-    std::lock_guard<std::mutex> lock(mu);
-    if (state[dev] == 0) {
-        hipDeviceProp_t prop;
-        e = hipGetDeviceProperties(&prop, dev);
-        if (e != hipSuccess) return hip_fail(e, "hipGetDeviceProperties");
-        state[dev] = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-        if (state[dev] == 2) {
-            return fail(MOE_ERR_UNSUPPORTED_DEVICE, "device %d is %s, this library is built for gfx950",
-                        dev, prop.gcnArchName);
-        }
-    }
-    if (state[dev] == 2) return fail(MOE_ERR_UNSUPPORTED_DEVICE, "device %d is not gfx950", dev);
     return MOE_OK;
 }
 

@@ -1,0 +1,405 @@
+// matmul.h -- the products of grouped_matmul, its gradients and linear: operands,
+// tile lookup, LDS staging and fragment reads shared by the kernels of
+// matmul128.hip and matmul256.hip.
+//
+// One launch computes, for every group e (rows offsets[e] .. offsets[e+1] - 1 of
+// the row operands; one group of P rows when offsets is null):
+//   kFwd  y[s]  = x[s] W_e^T               out [P, N], reduced over K
+//   kDx   dx[s] = dy[s] W_e                out [P, K], reduced over N
+//   kDw   dW_e  = sum_s dy[s]^T x[s]       out [E, N, K], reduced over the group's rows
+// with x [P, K], dy [P, N] and W [E, N, K] bf16 row-major, accumulated in fp32.
+//
+// As C[m][n] = sum_r A(m, r) B(n, r), an operand is stored either with r
+// contiguous (x and W of kFwd, dy of kDx) or with m / n contiguous (W of kDx, both
+// operands of kDw). Both kinds are staged by 16-byte global -> LDS loads whose
+// lanes cover whole 128-byte lines, and both are read as MFMA fragments without a
+// transposed copy: the first kind by 16-byte reads, the second by the transposing
+// 8-byte reads of gfx950 (16 lanes read 4 rows of 16 values and each gets a column).
+#pragma once
+
+#include "common.h"
+#include "train.h"
+
+namespace moe {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kStepR = 64;  // reduction depth of a staged step
+
+// 16 zero bytes: what a lane loads for a piece past the end of the reduction
+static __device__ __constant__ const uint32_t g_zero16[4] __attribute__((aligned(16))) = {0, 0, 0, 0};
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (const __attribute__((address_space(3))) void*)p));
+}
+
+// 16 bytes per lane from `src` (any lane's address) to LDS at dst + 16 * lane (dst
+// uniform over the wave), counted by vmcnt. In assembly because the compiler
+// waits for all such loads before any LDS read that it cannot tell apart from
+// their target, which would undo the prefetch; the kernels wait for them
+// themselves, with wait_loads and a barrier, before the stage is read. The load has no
+// destination register. m0 holds the LDS address; a write of it needs one wait
+// state before the load.
+__device__ __forceinline__ void lds_load16(const void* src, uint32_t dst) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :
+                 : "v"(src), "{m0}"(__builtin_amdgcn_readfirstlane(dst))
+                 : "memory");
+}
+// the same with the source as a uniform base and a 32-bit byte offset
+__device__ __forceinline__ void lds_load16(const uint8_t* base, uint32_t off, uint32_t dst) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(off), "s"(base), "{m0}"(__builtin_amdgcn_readfirstlane(dst))
+                 : "memory");
+}
+
+// Waits until at most N of this wave's loads to LDS are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// ---------------------------------------------------------------- tile lookup
+
+struct MatTile {
+    int group;
+    int64_t row0;  // first row (kFwd, kDx: of the row operand; kDw: of the group)
+    int nrows;     // rows of the tile (kDw: of the group)
+};
+
+// Rows of group e, clamped into [0, P]: offsets out of order or out of range give
+// wrong or empty groups, never an access outside the operands.
+__device__ __forceinline__ void group_rows(const MatmulArgs& a, int e, int64_t& first, int& count) {
+    if (!a.offsets) {
+        first = 0;
+        count = static_cast<int>(a.P);
+        return;
+    }
+    const int P = static_cast<int>(a.P);
+    int lo = a.offsets[e], hi = a.offsets[e + 1];
+    lo = lo < 0 ? 0 : lo > P ? P : lo;
+    hi = hi < lo ? lo : hi > P ? P : hi;
+    first = lo;
+    count = hi - lo;
+}
+
+// The row tiles of all groups, BM rows each, in group order: every wave scans
+// the group sizes by itself (four groups a lane, kMaxExperts in all), which needs
+// neither LDS nor a table written by an earlier launch.
+template <int BM>
+struct RowTiles {
+    int first[4], count[4], tiles[4];
+    int before;  // row tiles of the groups of lower lanes
+    int total;
+
+    __device__ __forceinline__ void scan(const MatmulArgs& a, int lane) {
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = 4 * lane + i;
+            first[i] = count[i] = tiles[i] = 0;
+            if (e < a.E) {
+                int64_t f;
+                group_rows(a, e, f, count[i]);
+                first[i] = static_cast<int>(f);
+                tiles[i] = (count[i] + BM - 1) / BM;
+            }
+            sum += tiles[i];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int v = __shfl_up(incl, off, kWave);
+            if (lane >= off) incl += v;
+        }
+        before = incl - sum;
+        total = __builtin_amdgcn_readlane(incl, 63);
+    }
+
+    // row tile rt < total
+    __device__ __forceinline__ MatTile find(int rt, int lane) const {
+        int local = rt - before, g = -1, f = 0, c = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (g < 0 && local >= 0 && local < tiles[i]) {
+                g = 4 * lane + i;
+                f = first[i] + local * BM;
+                c = count[i] - local * BM;
+            }
+            if (g < 0) local -= tiles[i];
+        }
+        const uint64_t hit = __ballot(g >= 0);
+        const int src = __builtin_amdgcn_readfirstlane(__ffsll(static_cast<unsigned long long>(hit)) - 1);
+        MatTile t;
+        t.group = __builtin_amdgcn_readlane(g, src);
+        t.row0 = __builtin_amdgcn_readlane(f, src);
+        const int left = __builtin_amdgcn_readlane(c, src);
+        t.nrows = left < BM ? left : BM;
+        return t;
+    }
+};
+
+// Block -> tile. Blocks are dealt to the 8 XCDs round robin, and each XCD takes
+// a contiguous range of the tiles, so that the tiles it runs at once share operand
+// panels in its L2. Inside a range the walk takes BAND row tiles down each column
+// of tiles before the next column.
+__device__ __forceinline__ bool xcd_slot(int64_t total, int64_t& lin) {
+    const int64_t xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+    const int64_t first = total * xcd / 8;
+    lin = first + slot;
+    return lin < total * (xcd + 1) / 8;
+}
+
+template <int BAND>
+__device__ __forceinline__ void band_walk(int64_t lin, int rows, int cols, int& rt, int& ct) {
+    const int64_t span = static_cast<int64_t>(BAND) * cols;
+    const int band = static_cast<int>(lin / span);
+    const int within = static_cast<int>(lin - band * span);
+    const int here = rows - band * BAND < BAND ? rows - band * BAND : BAND;
+    rt = band * BAND + within % here;
+    ct = within / here;
+}
+
+// ------------------------------------------------------------------- staging
+
+// LDS order of a tile stored with r contiguous, SIZE rows x 64 values: row-major,
+// 128 bytes a row, its eight 16-byte pieces XORed by spread(row). A 16-byte read
+// is served 16 lanes at a time over 64 banks (the lanes sharing lane bit 5 and
+// the parity of bits 2..4); with these spreads the 16 touch 16 different bank
+// groups. Rows of the first operand of a product (A) are read 16 consecutive ones
+// at a time; those of B in the order 16a + 4j + b for sub-tile j (below).
+template <bool PERMUTED>
+__device__ __forceinline__ int row_spread(int r) {
+    return PERMUTED ? (((r >> 1) & 1) | (((r >> 4) & 3) << 1)) : ((r >> 1) & 7);
+}
+
+// LDS order of a tile stored with m / n contiguous, 64 rows of r x SIZE values:
+// row-major, its 16-byte pieces XORed by this, so that the 16 rows which one
+// transposing read touches spread over all banks.
+__device__ __forceinline__ int red_spread(int r) { return (((r >> 3) & 3) << 2) | (r & 3); }
+
+// Global -> LDS staging of one operand's tile, 1 KB a wave and load.
+// TR: m / n contiguous. PERMUTED: rows read in sub-tile order (the B operand).
+template <bool TR, bool PERMUTED, int SIZE, int WAVES>
+struct Stager {
+    static constexpr int kLoads = SIZE / 8 / WAVES;  // per wave and step
+    static constexpr int kPieces = TR ? SIZE / 8 : 8;  // 16-byte pieces a tile row
+    static constexpr int kRows = 64 / kPieces;         // tile rows a load
+    const uint8_t* base;      // uniform: the tile's first value at step 0
+    int64_t step;             // bytes from step to step
+    uint32_t off[kLoads];     // this lane's source, relative to base
+    int wave, lane;
+
+    // TR = false: tile row i is row i of `p` (ld values apart), rows past `valid`
+    // repeat the last one. TR = true: tile row i is row i of the reduction, values
+    // past `valid` (a multiple of 8) repeat the last piece. What they give is dropped.
+    __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int valid, int wave_, int lane_) {
+        wave = wave_;
+        lane = lane_;
+        base = reinterpret_cast<const uint8_t*>(p);
+        step = TR ? kStepR * ld * 2 : kStepR * 2;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = tile_row(i);
+            if (TR) {
+                int c = piece(i) * 8;
+                c = c < valid ? c : valid - 8;
+                off[i] = static_cast<uint32_t>((r * ld + c) * 2);
+            } else {
+                off[i] = static_cast<uint32_t>(((r < valid ? r : valid - 1) * ld + piece(i) * 8) * 2);
+            }
+        }
+    }
+    __device__ __forceinline__ int tile_row(int i) const {
+        return (wave + i * WAVES) * kRows + lane / kPieces;
+    }
+    // the 16-byte piece of its row that this lane loads
+    __device__ __forceinline__ int piece(int i) const {
+        const int r = tile_row(i);
+        return (lane % kPieces) ^ (TR ? red_spread(r) : row_spread<PERMUTED>(r));
+    }
+    // loads [FROM, TO) of step k into the tile at LDS address `lds`; `red`: length of
+    // the reduction
+    template <int FROM = 0, int TO = kLoads>
+    __device__ __forceinline__ void load(uint32_t lds, int k, int64_t red) const {
+        const uint8_t* b = base + k * step;
+        const int64_t left = red - static_cast<int64_t>(k) * kStepR;
+        if (left >= kStepR) {
+#pragma unroll
+            for (int i = FROM; i < TO; ++i) lds_load16(b, off[i], lds + (wave + i * WAVES) * 1024);
+        } else {
+#pragma unroll
+            for (int i = FROM; i < TO; ++i) {
+                const int at = TR ? tile_row(i) : piece(i) * 8;
+                const void* src = at < left ? static_cast<const void*>(b + off[i])
+                                            : static_cast<const void*>(g_zero16);
+                lds_load16(src, lds + (wave + i * WAVES) * 1024);
+            }
+        }
+    }
+};
+
+// ---------------------------------------------------------------- fragments
+//
+// v_mfma_f32_16x16x32_bf16: lane l holds row l % 16, values 8 (l / 16) .. + 7 of
+// the 32-deep slice. B is passed first, so that D's rows are B's: lane l gets
+// D[4 (l / 16) + i][l % 16], i.e. four B rows of one A row. Sub-tile j of a wave's
+// 64 B rows takes the rows 16a + 4j + b (a, b = 0..3), so that a lane's values of
+// sub-tiles 0..3 are the 16 consecutive columns 16 (l / 16) .. + 15 of the output.
+
+// Reader of one operand's fragments from a tile at LDS address `base`.
+template <bool TR, bool PERMUTED, int SIZE>
+struct Reader {
+    int at[4];  // TR: byte address by sub-tile (A: i % 8 pairs; B: j >> 1); else by slice s
+    int first;
+
+    // row0: the wave's first row (m or n) in the tile, a multiple of 64
+    __device__ __forceinline__ void init(int row0, int lane) {
+        const int i16 = lane & 15, q = lane >> 4;
+        first = row0;
+        if (TR) {
+            // lane 4 j' + c of a 16-lane group reads row 8 q + j' (and + 4), values 4c .. 4c + 3
+            const int row = 8 * q + (i16 >> 2), c = i16 & 3;
+            const int g = red_spread(row);
+            if (PERMUTED) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    at[h] = row * SIZE * 2 + (((row0 / 8 + 2 * c + h) ^ g) * 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    at[i] = row * SIZE * 2 + (((row0 / 8 + 2 * i + (c >> 1)) ^ g) * 16) + (c & 1) * 8;
+            }
+        } else {
+            const int r = row0 + (PERMUTED ? 16 * (i16 >> 2) + (i16 & 3) : i16);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) at[s] = r * 128 + (((4 * s + q) ^ row_spread<PERMUTED>(r)) * 16);
+        }
+    }
+    // fragment of sub-tile i (0..3 of these 64 rows), slice s
+    __device__ __forceinline__ bf16x8 read(const uint8_t* lds, int i, int s) const {
+        if (TR) {
+            const uint8_t* p = lds + s * 32 * SIZE * 2 + (PERMUTED ? at[i >> 1] + (i & 1) * 8 : at[i]);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(p));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(p + 4 * SIZE * 2));
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+        return *reinterpret_cast<const bf16x8*>(lds + at[s] + i * (PERMUTED ? 4 : 16) * 128);
+    }
+};
+
+__device__ __forceinline__ f32x4 mfma_bf16(bf16x8 b, bf16x8 a, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------ epilogue
+
+__device__ __forceinline__ u32x4 pack8(const float* v) {
+    return u32x4{pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
+                 pack_bf16x2_rn(v[6], v[7])};
+}
+__device__ __forceinline__ void unpack8(u32x4 w, float* v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+// Eight consecutive values of output row `row` (index into the whole output),
+// columns col .. col + 7: bias, activation and residual (LINEAR), the old value
+// (accumulate), one rounding, one or two 16-byte stores.
+template <bool LINEAR>
+__device__ __forceinline__ void store8(const MatmulArgs& a, int64_t row, int64_t ld, int64_t col, float* v) {
+    const int64_t at = row * ld + col;
+    if (LINEAR) {
+        if (a.bias) {
+            const f32x4 b0 = *reinterpret_cast<const f32x4*>(a.bias + col);
+            const f32x4 b1 = *reinterpret_cast<const f32x4*>(a.bias + col + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] += b0[i];
+                v[4 + i] += b1[i];
+            }
+        }
+        if (a.z) *reinterpret_cast<u32x4*>(a.z + at) = pack8(v);
+        if (a.act != 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], a.act);
+        }
+        if (a.residual) {
+            float r[8];
+            unpack8(*reinterpret_cast<const u32x4*>(a.residual + at), r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += r[i];
+        }
+    }
+    if (a.out_fp32) {
+        float* o = static_cast<float*>(a.out) + at;
+        f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+        if (a.accumulate) {
+            lo += *reinterpret_cast<const f32x4*>(o);
+            hi += *reinterpret_cast<const f32x4*>(o + 4);
+        }
+        *reinterpret_cast<f32x4*>(o) = lo;
+        *reinterpret_cast<f32x4*>(o + 4) = hi;
+    } else {
+        uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+        if (a.accumulate) {
+            float old[8];
+            unpack8(*reinterpret_cast<const u32x4*>(o), old);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += old[i];
+        }
+        *reinterpret_cast<u32x4*>(o) = pack8(v);
+    }
+}
+
+// The operands of one tile as C[m][n] = sum_r A(m, r) B(n, r).
+template <int MODE>
+struct Operands {
+    const uint16_t *a, *b;  // at the tile's first row / column
+    int64_t lda, ldb;
+    int64_t red;            // length of the reduction
+    int rows, cols;         // valid rows and columns of the tile, from its origin
+    int64_t out_row, ldo, col0;
+};
+
+template <int MODE, int BM, int BN>
+__device__ __forceinline__ Operands<MODE> operands(const MatmulArgs& a, const MatTile& t, int rt, int ct) {
+    Operands<MODE> o;
+    o.col0 = static_cast<int64_t>(ct) * BN;
+    const int64_t ncols = (MODE == kFwd ? a.N : a.K) - o.col0;
+    o.cols = static_cast<int>(ncols < BN ? ncols : BN);
+    if (MODE == kDw) {
+        const int64_t m0 = static_cast<int64_t>(rt) * BM;
+        o.a = a.a + t.row0 * a.N + m0;
+        o.b = a.b + t.row0 * a.K + o.col0;
+        o.lda = a.N;
+        o.ldb = a.K;
+        o.red = t.nrows;
+        const int64_t nr = a.N - m0;
+        o.rows = static_cast<int>(nr < BM ? nr : BM);
+        o.out_row = t.group * a.N + m0;
+        o.ldo = a.K;
+    } else {
+        const int64_t kd = MODE == kFwd ? a.K : a.N;
+        const uint16_t* w = a.b + static_cast<int64_t>(t.group) * a.N * a.K;
+        o.a = a.a + t.row0 * kd;
+        o.b = MODE == kFwd ? w + o.col0 * a.K : w + o.col0;
+        o.lda = kd;
+        o.ldb = a.K;
+        o.red = kd;
+        o.rows = t.nrows;
+        o.out_row = t.row0;
+        o.ldo = MODE == kFwd ? a.N : a.K;
+    }
+    return o;
+}
+
+}  // namespace moe

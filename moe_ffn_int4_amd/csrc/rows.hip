@@ -1,0 +1,306 @@
+// rows.hip -- the row operators between the products: SwiGLU, the gradient through
+// an activation, and expert rows moved to and from their tokens. Each reads and
+// writes its operands once, in 16-byte pieces of 8 bf16 values; HBM bounds them all.
+#include "common.h"
+#include "train.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int NT = 256;
+
+__device__ __forceinline__ void load8(const uint16_t* p, float* v) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void load8(const float* p, float* v) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+    }
+}
+__device__ __forceinline__ void save8(uint16_t* p, const float* v) {
+    *reinterpret_cast<u32x4*>(p) = u32x4{pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
+                                         pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7])};
+}
+
+// Rows of `pieces` 16-byte pieces over blocks of 256 threads: 1 << shift threads a
+// row (a power of two covering the row, at most the block), chunks of a row across
+// blocks when it is longer.
+struct RowGrid {
+    int shift;
+    unsigned chunks;
+    unsigned blocks;
+    bool ok;
+};
+
+RowGrid row_grid(int64_t rows, int64_t pieces) {
+    RowGrid g;
+    g.shift = 0;
+    while ((1 << g.shift) < NT && (1 << g.shift) < pieces) ++g.shift;
+    g.chunks = static_cast<unsigned>((pieces + (1 << g.shift) - 1) >> g.shift);
+    const int64_t per = NT >> g.shift;
+    const int64_t blocks = (rows + per - 1) / per * g.chunks;
+    g.ok = blocks <= 0x7FFFFFFF;
+    g.blocks = static_cast<unsigned>(blocks);
+    return g;
+}
+
+// this thread's row and piece; false past the end
+__device__ __forceinline__ bool row_piece(int64_t rows, int64_t pieces, int shift, unsigned chunks,
+                                          int64_t& row, int64_t& piece) {
+    const unsigned b = blockIdx.x / chunks;
+    row = (static_cast<int64_t>(b) << (8 - shift)) + (threadIdx.x >> shift);
+    piece = (static_cast<int64_t>(blockIdx.x - b * chunks) << shift) + (threadIdx.x & ((1 << shift) - 1));
+    return row < rows && piece < pieces;
+}
+static_assert(NT == 256, "row_piece: 2^8 threads");
+
+}  // namespace
+
+// ------------------------------------------------------------------- SwiGLU
+
+__global__ __launch_bounds__(NT) void swiglu_kernel(const uint16_t* __restrict__ z, int64_t rows, int64_t h,
+                                                    int shift, unsigned chunks, uint16_t* __restrict__ y) {
+    int64_t r, c;
+    if (!row_piece(rows, h / 8, shift, chunks, r, c)) return;
+    float g[8], u[8];
+    load8(z + r * 2 * h + c * 8, g);
+    load8(z + r * 2 * h + h + c * 8, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = g[i] * sigmoid_rn(g[i]) * u[i];
+    save8(y + r * h + c * 8, g);
+}
+
+// dz may be z: a thread reads the two pieces that it then writes
+__global__ __launch_bounds__(NT) void swiglu_backward_kernel(const uint16_t* __restrict__ dy, const uint16_t* z,
+                                                             int64_t rows, int64_t h, int shift,
+                                                             unsigned chunks, uint16_t* dz) {
+    int64_t r, c;
+    if (!row_piece(rows, h / 8, shift, chunks, r, c)) return;
+    float d[8], g[8], u[8];
+    load8(dy + r * h + c * 8, d);
+    load8(z + r * 2 * h + c * 8, g);
+    load8(z + r * 2 * h + h + c * 8, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float s = sigmoid_rn(g[i]);
+        const float slope = act_slope(g[i], MOE_ACT_SILU);
+        u[i] = d[i] * u[i] * slope;
+        g[i] = d[i] * (g[i] * s);
+    }
+    save8(dz + r * 2 * h + c * 8, u);
+    save8(dz + r * 2 * h + h + c * 8, g);
+}
+
+hipError_t launch_swiglu(const uint16_t* z, int64_t rows, int64_t h, uint16_t* y, hipStream_t stream) {
+    const RowGrid g = row_grid(rows, h / 8);
+    if (!g.ok) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(swiglu_kernel, dim3(g.blocks), dim3(NT), 0, stream, z, rows, h, g.shift, g.chunks, y);
+    return hipGetLastError();
+}
+
+hipError_t launch_swiglu_backward(const uint16_t* dy, const uint16_t* z, int64_t rows, int64_t h,
+                                  uint16_t* dz, hipStream_t stream) {
+    const RowGrid g = row_grid(rows, h / 8);
+    if (!g.ok) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(swiglu_backward_kernel, dim3(g.blocks), dim3(NT), 0, stream, dy, z, rows, h, g.shift,
+                       g.chunks, dz);
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------ gradient of an activation
+
+// A block takes `rows` rows from blockIdx.y * rows and up to 64 pieces of columns;
+// lanes (a power of two covering the columns, at most 64) walk the columns and the
+// block's other threads the rows. Each thread sums its rows, the block its threads
+// in order, and dz_finish the slices in order.
+__global__ __launch_bounds__(NT) void linear_dz_kernel(const uint16_t* dy, const uint16_t* z, int act,
+                                                       int64_t T, int64_t N, int shift, int64_t rows,
+                                                       uint16_t* dz, float* __restrict__ sums) {
+    __shared__ float part[NT * 8];
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) << shift) + (threadIdx.x & ((1 << shift) - 1));
+    const int first = threadIdx.x >> shift, stride = NT >> shift;
+    const int64_t r0 = blockIdx.y * rows, r1 = r0 + rows < T ? r0 + rows : T;
+    float sum[8] = {};
+    if (c * 8 < N) {
+        for (int64_t r = r0 + first; r < r1; r += stride) {
+            float d[8];
+            load8(dy + r * N + c * 8, d);
+            if (act != MOE_ACT_NONE) {
+                float v[8];
+                load8(z + r * N + c * 8, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] *= act_slope(v[i], act);
+                save8(dz + r * N + c * 8, d);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += d[i];
+        }
+    }
+    if (!sums) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[threadIdx.x * 8 + i] = sum[i];
+    __syncthreads();
+    // thread -> one column of the block's 8 << shift; a loop because there may be
+    // more columns than threads
+    for (int col = threadIdx.x; col < (8 << shift); col += NT) {
+        const int64_t at = (static_cast<int64_t>(blockIdx.x) << (shift + 3)) + col;
+        if (at >= N) break;
+        float s = 0.f;
+        for (int i = 0; i < stride; ++i) s += part[(i << (shift + 3)) + col];
+        sums[blockIdx.y * N + at] = s;
+    }
+}
+
+__global__ __launch_bounds__(NT) void dz_finish_kernel(const float* __restrict__ partial, int64_t slices,
+                                                       int64_t N, float* __restrict__ db) {
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x;
+    if (c >= N) return;
+    float s = 0.f;
+    for (int64_t i = 0; i < slices; ++i) s += partial[i * N + c];
+    db[c] = s;
+}
+
+constexpr int64_t kDzRows = 128;
+constexpr int64_t kDzMaxSlices = 1024;
+
+int64_t linear_dz_slices(int64_t T, int64_t N) {
+    int64_t s = (T + kDzRows - 1) / kDzRows;
+    return s < 1 ? 1 : s > kDzMaxSlices ? kDzMaxSlices : s;
+}
+
+hipError_t launch_linear_dz(const uint16_t* dy, const uint16_t* z, int act, int64_t T, int64_t N,
+                            uint16_t* dz, float* db, float* partial, hipStream_t stream) {
+    const int64_t slices = linear_dz_slices(T, N);
+    const int64_t rows = (T + slices - 1) / slices;
+    int shift = 0;
+    while ((1 << shift) < 64 && (8 << shift) < N) ++shift;
+    const int64_t cols = (N + (8 << shift) - 1) >> (shift + 3);
+    float* sums = !db ? nullptr : slices == 1 ? db : partial;
+    hipLaunchKernelGGL(linear_dz_kernel, dim3(static_cast<unsigned>(cols), static_cast<unsigned>(slices)),
+                       dim3(NT), 0, stream, dy, z, act, T, N, shift, rows, dz, sums);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !db || slices == 1) return e;
+    hipLaunchKernelGGL(dz_finish_kernel, dim3(static_cast<unsigned>((N + NT - 1) / NT)), dim3(NT), 0, stream,
+                       partial, slices, N, db);
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------ expert row movement
+
+__global__ __launch_bounds__(NT) void permute_rows_kernel(const uint16_t* __restrict__ x,
+                                                          const int32_t* __restrict__ perm, int64_t T,
+                                                          int top_k, int64_t d, int shift, unsigned chunks,
+                                                          uint16_t* __restrict__ xp) {
+    int64_t s, c;
+    if (!row_piece(T * top_k, d / 8, shift, chunks, s, c)) return;
+    const int pair = perm[s];
+    u32x4 v = {0, 0, 0, 0};  // a pair outside [0, T * top_k) gives a row of zeros
+    if (pair >= 0 && pair < T * top_k)
+        v = *reinterpret_cast<const u32x4*>(x + static_cast<int64_t>(pair / top_k) * d + c * 8);
+    *reinterpret_cast<u32x4*>(xp + s * d + c * 8) = v;
+}
+
+template <typename O>
+__global__ __launch_bounds__(NT) void combine_rows_kernel(const O* __restrict__ o,
+                                                          const int32_t* __restrict__ inv,
+                                                          const float* __restrict__ gates,
+                                                          const uint16_t* residual, int64_t T, int top_k,
+                                                          int64_t d, int shift, unsigned chunks, uint16_t* y) {
+    int64_t t, c;
+    if (!row_piece(T, d / 8, shift, chunks, t, c)) return;
+    float acc[8] = {};
+    if (residual) load8(residual + t * d + c * 8, acc);
+    for (int j = 0; j < top_k; ++j) {
+        const int slot = inv[t * top_k + j];
+        if (slot < 0 || slot >= T * top_k) continue;
+        const float g = gates ? gates[t * top_k + j] : 1.0f;
+        float v[8];
+        load8(o + static_cast<int64_t>(slot) * d + c * 8, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(g, v[i], acc[i]);
+    }
+    save8(y + t * d + c * 8, acc);
+}
+
+// One wave for each (token, j): d_o[slot] = g dy[t] and d_gates[t, j] = <dy[t], o[slot]>.
+template <typename O>
+__global__ __launch_bounds__(NT) void combine_backward_kernel(const uint16_t* __restrict__ dy,
+                                                              const O* __restrict__ o,
+                                                              const int32_t* __restrict__ inv,
+                                                              const float* __restrict__ gates, int64_t T,
+                                                              int top_k, int64_t d,
+                                                              uint16_t* __restrict__ d_o,
+                                                              float* __restrict__ d_gates) {
+    const int64_t pair = static_cast<int64_t>(blockIdx.x) * (NT / 64) + (threadIdx.x >> 6);
+    if (pair >= T * top_k) return;
+    const int lane = threadIdx.x & 63;
+    const int64_t t = pair / top_k;
+    const int slot = inv[pair];
+    const bool in = slot >= 0 && slot < T * top_k;
+    const float g = gates ? gates[pair] : 1.0f;
+    float dot = 0.f;
+    for (int64_t c = lane; in && c < d / 8; c += 64) {
+        float v[8], w[8];
+        load8(dy + t * d + c * 8, v);
+        if (d_gates) {
+            load8(o + static_cast<int64_t>(slot) * d + c * 8, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dot = fmaf(v[i], w[i], dot);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= g;
+        save8(d_o + static_cast<int64_t>(slot) * d + c * 8, v);
+    }
+    if (!d_gates) return;
+    dot = wave_sum(dot);
+    if (lane == 0) d_gates[pair] = dot;
+}
+
+hipError_t launch_permute_rows(const uint16_t* x, const int32_t* perm, int64_t T, int top_k, int64_t d,
+                               uint16_t* xp, hipStream_t stream) {
+    const RowGrid g = row_grid(T * top_k, d / 8);
+    if (!g.ok) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(permute_rows_kernel, dim3(g.blocks), dim3(NT), 0, stream, x, perm, T, top_k, d, g.shift,
+                       g.chunks, xp);
+    return hipGetLastError();
+}
+
+hipError_t launch_combine_rows(const void* o, bool o_fp32, const int32_t* inv, const float* gates,
+                               const uint16_t* residual, int64_t T, int top_k, int64_t d, uint16_t* y,
+                               hipStream_t stream) {
+    const RowGrid g = row_grid(T, d / 8);
+    if (!g.ok) return hipErrorInvalidConfiguration;
+    if (o_fp32)
+        hipLaunchKernelGGL(combine_rows_kernel<float>, dim3(g.blocks), dim3(NT), 0, stream,
+                           static_cast<const float*>(o), inv, gates, residual, T, top_k, d, g.shift, g.chunks, y);
+    else
+        hipLaunchKernelGGL(combine_rows_kernel<uint16_t>, dim3(g.blocks), dim3(NT), 0, stream,
+                           static_cast<const uint16_t*>(o), inv, gates, residual, T, top_k, d, g.shift, g.chunks, y);
+    return hipGetLastError();
+}
+
+hipError_t launch_combine_backward(const uint16_t* dy, const void* o, bool o_fp32, const int32_t* inv,
+                                   const float* gates, int64_t T, int top_k, int64_t d, uint16_t* d_o,
+                                   float* d_gates, hipStream_t stream) {
+    const int64_t blocks = (T * top_k + NT / 64 - 1) / (NT / 64);
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(blocks));
+    if (o_fp32)
+        hipLaunchKernelGGL(combine_backward_kernel<float>, grid, dim3(NT), 0, stream, dy,
+                           static_cast<const float*>(o), inv, gates, T, top_k, d, d_o, d_gates);
+    else
+        hipLaunchKernelGGL(combine_backward_kernel<uint16_t>, grid, dim3(NT), 0, stream, dy,
+                           static_cast<const uint16_t*>(o), inv, gates, T, top_k, d, d_o, d_gates);
+    return hipGetLastError();
+}
+
+}  // namespace moe
