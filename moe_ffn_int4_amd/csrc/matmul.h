@@ -1,6 +1,6 @@
 // matmul.h -- the products of grouped_matmul, its gradients and linear: operands,
 // tile lookup, LDS staging and fragment reads shared by the kernels of
-// matmul128.hip and matmul256.hip.
+// matmul_tile.hip, matmul256.hip and matmul_stream.hip.
 //
 // One launch computes, for every group e (rows offsets[e] .. offsets[e+1] - 1 of
 // the row operands; one group of P rows when offsets is null):
@@ -146,13 +146,6 @@ struct RowTiles {
 // a contiguous range of the tiles, so that the tiles it runs at once share operand
 // panels in its L2. Inside a range the walk takes BAND row tiles down each column
 // of tiles before the next column.
-__device__ __forceinline__ bool xcd_slot(int64_t total, int64_t& lin) {
-    const int64_t xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-    const int64_t first = total * xcd / 8;
-    lin = first + slot;
-    return lin < total * (xcd + 1) / 8;
-}
-
 template <int BAND>
 __device__ __forceinline__ void band_walk(int64_t lin, int rows, int cols, int& rt, int& ct) {
     const int64_t span = static_cast<int64_t>(BAND) * cols;
@@ -163,27 +156,81 @@ __device__ __forceinline__ void band_walk(int64_t lin, int rows, int cols, int& 
     ct = within / here;
 }
 
-// ------------------------------------------------------------------- staging
-
-// LDS order of a tile stored with r contiguous, SIZE rows x 64 values: row-major,
-// 128 bytes a row, its eight 16-byte pieces XORed by spread(row). A 16-byte read
-// is served 16 lanes at a time over 64 banks (the lanes sharing lane bit 5 and
-// the parity of bits 2..4); with these spreads the 16 touch 16 different bank
-// groups. Rows of the first operand of a product (A) are read 16 consecutive ones
-// at a time; those of B in the order 16a + 4j + b for sub-tile j (below).
-template <bool PERMUTED>
-__device__ __forceinline__ int row_spread(int r) {
-    return PERMUTED ? (((r >> 1) & 1) | (((r >> 4) & 3) << 1)) : ((r >> 1) & 7);
+// The tile of this block; false: none. kDw: every group has the same tiles. Where they
+// are many, each XCD takes a contiguous eighth of each group's, so that groups of
+// unequal length weigh equally on all; else it takes an eighth of all groups' tiles.
+constexpr int64_t kManyTiles = 64;
+template <int MODE, int BM, int BN, int BAND>
+__device__ __forceinline__ bool find_tile(const MatmulArgs& a, int lane, MatTile& t, int& rt, int& ct) {
+    const int ncol = static_cast<int>(((MODE == kFwd ? a.N : a.K) + BN - 1) / BN);
+    const int xcd = blockIdx.x & 7;
+    int64_t lin = blockIdx.x >> 3;
+    if (MODE == kDw) {
+        const int nrow = static_cast<int>((a.N + BM - 1) / BM);
+        const int64_t n = static_cast<int64_t>(nrow) * ncol;
+        const int64_t all = n < kManyTiles ? n * a.E : n;
+        const int64_t first = all * xcd / 8, mine = all * (xcd + 1) / 8 - first;
+        if (lin >= (n < kManyTiles ? mine : mine * a.E)) return false;
+        if (n < kManyTiles) {
+            t.group = static_cast<int>((first + lin) / n);
+            lin = first + lin - t.group * n;
+        } else {
+            t.group = static_cast<int>(lin / mine);
+            lin = first + lin - t.group * mine;
+        }
+        band_walk<BAND>(lin, nrow, ncol, rt, ct);
+        group_rows(a, t.group, t.row0, t.nrows);
+        return !(a.accumulate && t.nrows == 0);
+    }
+    RowTiles<BM> tiles;
+    tiles.scan(a, lane);
+    const int64_t n = static_cast<int64_t>(tiles.total) * ncol;
+    const int64_t first = n * xcd / 8, mine = n * (xcd + 1) / 8 - first;
+    if (lin >= mine) return false;
+    band_walk<BAND>(first + lin, tiles.total, ncol, rt, ct);
+    t = tiles.find(rt, lane);
+    return true;
 }
 
+// Blocks of a launch, an upper bound: the host does not know the group sizes.
+template <int MODE, int BM, int BN>
+inline int64_t matmul_blocks(const MatmulArgs& a) {
+    const int64_t ncol = ((MODE == kFwd ? a.N : a.K) + BN - 1) / BN;
+    int64_t mine;  // the most tiles of an XCD
+    if (MODE == kDw) {
+        const int64_t n = ((a.N + BM - 1) / BM) * ncol;
+        mine = n < kManyTiles ? (a.E * n + 7) / 8 : a.E * ((n + 7) / 8);
+    } else {
+        // row tiles: full ones and at most one partial tile for each group with rows
+        const int64_t partial = a.E < a.P ? a.E : a.P;
+        mine = ((a.P / BM + partial) * ncol + 7) / 8;
+    }
+    return 8 * mine;
+}
+
+// ------------------------------------------------------------------- staging
+
+// LDS order of a tile stored with r contiguous, rows of 64 values: row-major, 128
+// bytes a row, its eight 16-byte pieces XORed by row_spread. A 16-byte read is
+// served 16 lanes at a time over 64 banks (the lanes sharing lane bit 5 and
+// the parity of bits 2..4); reading 16 rows in a row, the 16 touch 16 different
+// groups of four banks.
+__device__ __forceinline__ int row_spread(int r) { return (r >> 1) & 7; }
+
 // LDS order of a tile stored with m / n contiguous, 64 rows of r x SIZE values:
-// row-major, its 16-byte pieces XORed by this, so that the 16 rows which one
-// transposing read touches spread over all banks.
-__device__ __forceinline__ int red_spread(int r) { return (((r >> 3) & 3) << 2) | (r & 3); }
+// row-major, 2 SIZE bytes a row, its 16-byte pieces XORed by red_spread. A transposing
+// 8-byte read is served 32 lanes at a time: 8 rows (four in a row, twice, 8 apart)
+// of 32 bytes each, which the even XOR values put on 16 different groups of four banks
+// (with rows of 128 bytes the lowest bit of the row does its part).
+template <int SIZE>
+__device__ __forceinline__ int red_spread(int r) {
+    if (SIZE == 64) return (((r >> 3) & 1) << 2) | (r & 2);
+    return (((r >> 3) & 1) << 3) | ((r & 3) << 1);
+}
 
 // Global -> LDS staging of one operand's tile, 1 KB a wave and load.
-// TR: m / n contiguous. PERMUTED: rows read in sub-tile order (the B operand).
-template <bool TR, bool PERMUTED, int SIZE, int WAVES>
+// TR: m / n contiguous.
+template <bool TR, int SIZE, int WAVES>
 struct Stager {
     static constexpr int kLoads = SIZE / 8 / WAVES;  // per wave and step
     static constexpr int kPieces = TR ? SIZE / 8 : 8;  // 16-byte pieces a tile row
@@ -219,7 +266,7 @@ struct Stager {
     // the 16-byte piece of its row that this lane loads
     __device__ __forceinline__ int piece(int i) const {
         const int r = tile_row(i);
-        return (lane % kPieces) ^ (TR ? red_spread(r) : row_spread<PERMUTED>(r));
+        return (lane % kPieces) ^ (TR ? red_spread<SIZE>(r) : row_spread(r));
     }
     // loads [FROM, TO) of step k into the tile at LDS address `lds`; `red`: length of
     // the reduction
@@ -246,50 +293,40 @@ struct Stager {
 //
 // v_mfma_f32_16x16x32_bf16: lane l holds row l % 16, values 8 (l / 16) .. + 7 of
 // the 32-deep slice. B is passed first, so that D's rows are B's: lane l gets
-// D[4 (l / 16) + i][l % 16], i.e. four B rows of one A row. Sub-tile j of a wave's
-// 64 B rows takes the rows 16a + 4j + b (a, b = 0..3), so that a lane's values of
-// sub-tiles 0..3 are the 16 consecutive columns 16 (l / 16) .. + 15 of the output.
+// D[4 (l / 16) + i][l % 16], i.e. four consecutive columns of the output in one row.
 
-// Reader of one operand's fragments from a tile at LDS address `base`.
-template <bool TR, bool PERMUTED, int SIZE>
+// Reader of one operand's fragments from a tile of SIZE values of m / n.
+template <bool TR, int SIZE>
 struct Reader {
-    int at[4];  // TR: byte address by sub-tile (A: i % 8 pairs; B: j >> 1); else by slice s
-    int first;
+    static constexpr int kSubs = SIZE == 64 ? 2 : 4;
+    int at[TR ? kSubs : 2];  // byte address, TR: by sub-tile, else by slice s
 
-    // row0: the wave's first row (m or n) in the tile, a multiple of 64
+    // row0: the wave's first row (m or n) in the tile, a multiple of 32
     __device__ __forceinline__ void init(int row0, int lane) {
         const int i16 = lane & 15, q = lane >> 4;
-        first = row0;
         if (TR) {
-            // lane 4 j' + c of a 16-lane group reads row 8 q + j' (and + 4), values 4c .. 4c + 3
+            // lane 4 j + c of a 16-lane group reads row 8 q + j (and + 4), values 4c .. 4c + 3
             const int row = 8 * q + (i16 >> 2), c = i16 & 3;
-            const int g = red_spread(row);
-            if (PERMUTED) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    at[h] = row * SIZE * 2 + (((row0 / 8 + 2 * c + h) ^ g) * 16);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    at[i] = row * SIZE * 2 + (((row0 / 8 + 2 * i + (c >> 1)) ^ g) * 16) + (c & 1) * 8;
-            }
+            for (int i = 0; i < kSubs; ++i)
+                at[i] = row * SIZE * 2 + (((row0 / 8 + 2 * i + (c >> 1)) ^ red_spread<SIZE>(row)) * 16) + (c & 1) * 8;
         } else {
-            const int r = row0 + (PERMUTED ? 16 * (i16 >> 2) + (i16 & 3) : i16);
+            const int r = row0 + i16;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) at[s] = r * 128 + (((4 * s + q) ^ row_spread<PERMUTED>(r)) * 16);
+            for (int s = 0; s < 2; ++s) at[s] = r * 128 + (((4 * s + q) ^ row_spread(r)) * 16);
         }
     }
-    // fragment of sub-tile i (0..3 of these 64 rows), slice s
+    // fragment of sub-tile i (rows row0 + 16 i ..; i < 4), slice s
     __device__ __forceinline__ bf16x8 read(const uint8_t* lds, int i, int s) const {
         if (TR) {
-            const uint8_t* p = lds + s * 32 * SIZE * 2 + (PERMUTED ? at[i >> 1] + (i & 1) * 8 : at[i]);
+            const uint8_t* p = lds + s * 32 * SIZE * 2 + at[i];
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (__attribute__((address_space(3))) s16x4*)(p));
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (__attribute__((address_space(3))) s16x4*)(p + 4 * SIZE * 2));
             return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         }
-        return *reinterpret_cast<const bf16x8*>(lds + at[s] + i * (PERMUTED ? 4 : 16) * 128);
+        return *reinterpret_cast<const bf16x8*>(lds + at[s] + i * 16 * 128);
     }
 };
 
@@ -310,6 +347,19 @@ __device__ __forceinline__ void unpack8(u32x4 w, float* v) {
         v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
+
+// Two neighbouring sub-tiles' four columns a lane -> eight consecutive columns:
+// lane groups q and q ^ 1 exchange halves, after which group q holds the columns
+// 16 (q % 2) + 8 (q / 2) .. + 7 of the pair's 32.
+__device__ __forceinline__ void eight_columns(f32x4 x, f32x4 y, float* v) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x[r]), __float_as_uint(y[r]), false, false);
+        v[r] = __uint_as_float(p[0]);
+        v[4 + r] = __uint_as_float(p[1]);
+    }
+}
+__device__ __forceinline__ int eight_columns_at(int q) { return 16 * (q & 1) + 8 * (q >> 1); }
 
 // Eight consecutive values of output row `row` (index into the whole output),
 // columns col .. col + 7: bias, activation and residual (LINEAR), the old value
@@ -360,6 +410,20 @@ __device__ __forceinline__ void store8(const MatmulArgs& a, int64_t row, int64_t
     }
 }
 
+// The same for one value.
+template <bool LINEAR>
+__device__ __forceinline__ void store1(const MatmulArgs& a, int64_t row, int64_t ld, int64_t col, float v) {
+    const int64_t at = row * ld + col;
+    if (LINEAR) {
+        if (a.bias) v += a.bias[col];
+        if (a.z) a.z[at] = static_cast<uint16_t>(pack_bf16x2_rn(v, 0.f));
+        v = act_value(v, a.act);
+        if (a.residual) v += bf16_to_f32(a.residual[at]);
+    }
+    if (a.out_fp32) static_cast<float*>(a.out)[at] = v;
+    else static_cast<uint16_t*>(a.out)[at] = static_cast<uint16_t>(pack_bf16x2_rn(v, 0.f));
+}
+
 // The operands of one tile as C[m][n] = sum_r A(m, r) B(n, r).
 template <int MODE>
 struct Operands {
@@ -370,33 +434,38 @@ struct Operands {
     int64_t out_row, ldo, col0;
 };
 
+// part: 0 or 1 for the first or last BM / 2 rows of the tile, -1 for all; `rows` is not
+// positive for a half that has none
 template <int MODE, int BM, int BN>
-__device__ __forceinline__ Operands<MODE> operands(const MatmulArgs& a, const MatTile& t, int rt, int ct) {
+__device__ __forceinline__ Operands<MODE> operands(const MatmulArgs& a, const MatTile& t, int rt, int ct,
+                                                   int part) {
+    const int skip = part > 0 ? BM / 2 : 0, most = part < 0 ? BM : BM / 2;
     Operands<MODE> o;
     o.col0 = static_cast<int64_t>(ct) * BN;
     const int64_t ncols = (MODE == kFwd ? a.N : a.K) - o.col0;
     o.cols = static_cast<int>(ncols < BN ? ncols : BN);
     if (MODE == kDw) {
-        const int64_t m0 = static_cast<int64_t>(rt) * BM;
+        const int64_t m0 = static_cast<int64_t>(rt) * BM + skip;
         o.a = a.a + t.row0 * a.N + m0;
         o.b = a.b + t.row0 * a.K + o.col0;
         o.lda = a.N;
         o.ldb = a.K;
         o.red = t.nrows;
         const int64_t nr = a.N - m0;
-        o.rows = static_cast<int>(nr < BM ? nr : BM);
+        o.rows = static_cast<int>(nr < most ? nr : most);
         o.out_row = t.group * a.N + m0;
         o.ldo = a.K;
     } else {
         const int64_t kd = MODE == kFwd ? a.K : a.N;
         const uint16_t* w = a.b + static_cast<int64_t>(t.group) * a.N * a.K;
-        o.a = a.a + t.row0 * kd;
+        const int64_t row0 = t.row0 + skip;
+        o.a = a.a + row0 * kd;
         o.b = MODE == kFwd ? w + o.col0 * a.K : w + o.col0;
         o.lda = kd;
         o.ldb = a.K;
         o.red = kd;
-        o.rows = t.nrows;
-        o.out_row = t.row0;
+        o.rows = t.nrows - skip < most ? t.nrows - skip : most;
+        o.out_row = row0;
         o.ldo = MODE == kFwd ? a.N : a.K;
     }
     return o;

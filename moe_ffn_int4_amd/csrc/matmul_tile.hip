@@ -1,0 +1,160 @@
+// matmul_tile.hip -- the products of matmul.h in square tiles of 128 or 64, for outputs
+// that do not fill the chip with 256 x 256 tiles, and the choice of the kernel.
+//
+// One block of 4 waves in a 2 x 2 grid, each a quarter of the tile. The reduction runs
+// in 64-deep steps through a ring of LDS stages: step k + RING - 1 is requested, straight
+// to LDS, while step k is multiplied, one barrier a step. With 64 KB of LDS two blocks
+// share a CU, and one block's loads and barriers overlap the other's products.
+#include "matmul.h"
+
+namespace moe {
+
+namespace {
+constexpr int kWaves = 4;
+constexpr int kBand = 8;  // row tiles walked down a column of tiles
+
+// at most `steps` of the youngest steps' requests (PER a wave each) left in flight
+template <int PER, int MOST>
+__device__ __forceinline__ void wait_steps(int steps) {
+    if constexpr (MOST == 0) {
+        wait_loads<0>();
+    } else {
+        if (steps >= MOST) wait_loads<PER * MOST>();
+        else wait_steps<PER, MOST - 1>(steps);
+    }
+}
+}  // namespace
+
+template <int MODE, bool LINEAR, int T, int RING>
+__global__ __launch_bounds__(64 * kWaves, 2) void matmul_tile_kernel(MatmulArgs a) {
+    constexpr int kTile = T * kStepR * 2;  // one operand of one step
+    constexpr int kStage = 2 * kTile;
+    constexpr int S = T / 32;              // 16-wide sub-tiles of a wave, each way
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    MatTile t;
+    int rt, ct;
+    if (!find_tile<MODE, T, T, kBand>(a, lane, t, rt, ct)) return;
+    const Operands<MODE> o = operands<MODE, T, T>(a, t, rt, ct, -1);
+
+    constexpr bool AT = MODE == kDw, BT = MODE != kFwd;
+    Stager<AT, T, kWaves> sa;
+    Stager<BT, T, kWaves> sb;
+    sa.init(o.a, o.lda, o.rows, wave, lane);
+    sb.init(o.b, o.ldb, o.cols, wave, lane);
+    const int wm = (wave >> 1) * (T / 2), wn = (wave & 1) * (T / 2);
+    Reader<AT, T> ra;
+    Reader<BT, T> rb;
+    ra.init(wm, lane);
+    rb.init(wn, lane);
+
+    f32x4 acc[S][S];
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+        for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int steps = static_cast<int>((o.red + kStepR - 1) / kStepR);
+    const uint32_t at = lds_address(lds);
+    constexpr int kLoads = 2 * T / 8 / kWaves;  // a wave's, a step
+    auto request = [&](int stage, int k) __attribute__((always_inline)) {
+        sa.load(at + stage * kStage, k, o.red);
+        sb.load(at + stage * kStage + kTile, k, o.red);
+    };
+    for (int k = 0; k < RING - 1 && k < steps; ++k) request(k, k);
+    int cur = 0, next = RING - 1;  // stages of step k and of step k + RING - 1
+    for (int k = 0; k < steps; ++k) {
+        // step k has landed (steps k + 1 .. k + RING - 2 may be under way), and every
+        // wave has read step k - 1, whose stage is the next to be written
+        wait_steps<kLoads, RING - 2>(steps - 1 - k);
+        __syncthreads();
+        if (k + RING - 1 < steps) request(next, k + RING - 1);
+        const uint8_t* p = lds + cur * kStage;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            bf16x8 fa[S], fb[S];
+#pragma unroll
+            for (int i = 0; i < S; ++i) fa[i] = ra.read(p, i, s);
+#pragma unroll
+            for (int j = 0; j < S; ++j) fb[j] = rb.read(p + kTile, j, s);
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+                for (int j = 0; j < S; ++j) acc[i][j] = mfma_bf16(fb[j], fa[i], acc[i][j]);
+        }
+        cur = cur == RING - 1 ? 0 : cur + 1;
+        next = next == RING - 1 ? 0 : next + 1;
+    }
+
+    const int i16 = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        const int row = wm + 16 * i + i16;
+#pragma unroll
+        for (int h = 0; h < S / 2; ++h) {
+            float v[8];
+            eight_columns(acc[i][2 * h], acc[i][2 * h + 1], v);
+            const int col = wn + 32 * h + eight_columns_at(q);
+            if (row < o.rows && col < o.cols) store8<LINEAR>(a, o.out_row + row, o.ldo, o.col0 + col, v);
+        }
+    }
+}
+
+template <int MODE, bool LINEAR, int T, int RING>
+static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
+    constexpr int kLds = RING * 2 * T * kStepR * 2;
+    static const hipError_t ready = hipFuncSetAttribute(
+        reinterpret_cast<const void*>(&matmul_tile_kernel<MODE, LINEAR, T, RING>),
+        hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (ready != hipSuccess) return ready;
+    const int64_t blocks = matmul_blocks<MODE, T, T>(a);
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((matmul_tile_kernel<MODE, LINEAR, T, RING>), dim3(static_cast<unsigned>(blocks)),
+                       dim3(64 * kWaves), kLds, stream, a);
+    return hipGetLastError();
+}
+
+template <int T, int RING>
+static hipError_t launch_tile(int mode, bool linear, const MatmulArgs& a, hipStream_t stream) {
+    if (mode == kDx) return launch<kDx, false, T, RING>(a, stream);
+    if (mode == kDw) return launch<kDw, false, T, RING>(a, stream);
+    return linear ? launch<kFwd, true, T, RING>(a, stream) : launch<kFwd, false, T, RING>(a, stream);
+}
+
+// Tiles of T x T, an estimate where the host does not know the group sizes: each
+// group's last row tile is half empty.
+static int64_t tiles(int mode, const MatmulArgs& a, int64_t T) {
+    auto up = [T](int64_t v) { return (v + T - 1) / T; };
+    if (mode == kDw) return a.E * up(a.N) * up(a.K);
+    const int64_t groups = a.E < a.P ? a.E : a.P;
+    const int64_t rows = groups == 1 ? up(a.P) : a.P / T + (groups + 1) / 2;
+    return rows * up(mode == kFwd ? a.N : a.K);
+}
+
+// The kernel for a product. What decides is how many tiles there are for the chip's
+// 256 CUs, and (us, measured at rows x N x K, dense unless E experts are named):
+//   * few rows, y = x W^T: the streaming kernel. 1 x 8192 x 5120: 17 against 29 in tiles
+//     of 64; 16 rows: 19 against 29; 32 rows: 29 against 30. 16 rows over E = 16 of
+//     16384 x 5120: 424 against 434 in tiles of 256; 64 rows: 461 against 434.
+//   * up to 512 tiles of 64: those. 64 x 8192 x 5120: 32 (128: 58, 256: 85); 256 x 8192 x
+//     5120 (512 tiles): 53 (63, 89); 512 x 8192 x 5120 (1024): 92 (66, 86); 2048 x 1024 x
+//     1024 (512): 14 (21, 25).
+//   * up to 256 tiles of 128: those, one block a CU, over four stages (three steps
+//     ahead; two stages and two blocks: 81). 512 x 8192 x 5120 (256): 66; 1024 x 8192 x
+//     5120 (512): 124 against 92 in tiles of 256.
+//   * weight gradients of short reductions, whose time is the stores: tiles of 128,
+//     two blocks a CU. 20 rows in each of E = 128, 1000 x 712: 44 (256: 49); 64 rows in
+//     each of E = 8, 2048 x 1024: 10 (14); 512 rows in each of E = 16, 5120 x 8192: 834
+//     against 770 in tiles of 256.
+//   * else tiles of 256. 4096 x 2048 x 1024 (128): 29 (128: 30); 1024 x 5120 x 8192 (80):
+//     115 (132).
+hipError_t launch_matmul(int mode, bool linear, const MatmulArgs& a, hipStream_t stream) {
+    if (mode == kFwd && (a.P <= 16 || a.P <= 4 * a.E)) return launch_matmul_stream(linear, a, stream);
+    if (tiles(mode, a, 64) <= 512) return launch_tile<64, 4>(mode, linear, a, stream);
+    if (tiles(mode, a, 128) <= 256) return launch_tile<128, 4>(mode, linear, a, stream);
+    if (mode == kDw && a.P < 384 * a.E) return launch<kDw, false, 128, 2>(a, stream);
+    return launch_matmul256(mode, linear, a, stream);
+}
+
+}  // namespace moe

@@ -33,7 +33,8 @@ struct MatmulArgs {
     int act;                 // MOE_ACT_*
 };
 
-hipError_t launch_matmul128(int mode, bool linear, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_matmul256(int mode, bool linear, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_matmul_stream(bool linear, const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_matmul(int mode, bool linear, const MatmulArgs& a, hipStream_t stream);
 
 // two fp32 -> packed bf16 pair, round to nearest even, NaN kept

@@ -8,8 +8,9 @@ from train_util import DEV, HALF, bf16, gen, offsets_of, product_bound, say, spl
 pytestmark = pytest.mark.gpu
 OUT = [torch.bfloat16, torch.float32]
 
-# (P, E, N, K, skew, empty groups): one row up to several tiles of every kernel, widths
-# that end inside a tile, a step or a 16-wide sub-tile, groups without rows
+# (P, E, N, K, skew, empty groups): one row up to several tiles of every kernel (the
+# streaming one, tiles of 64, 128 and 256, blocks that do several tiles, tiles cut in
+# two), widths that end inside a tile, a step or a 16-wide sub-tile, groups without rows
 SHAPES = [
     (1, 1, 8, 8, 0.0, ()),
     (5, 3, 16, 24, 0.0, (1,)),
@@ -21,6 +22,15 @@ SHAPES = [
     (700, 2, 392, 328, 0.0, ()),
     (1500, 5, 776, 1032, 1.0, (2,)),
     (0, 4, 16, 40, 0.0, ()),
+    (1500, 2, 1704, 136, 0.0, ()),
+    (1500, 2, 136, 1704, 0.0, ()),
+    (700, 40, 392, 328, 1.0, (3,)),
+    (2100, 3, 2600, 200, 0.5, ()),
+    (2100, 3, 200, 2600, 0.5, ()),
+    (1300, 3, 1400, 1096, 0.0, ()),
+    (9000, 1, 2104, 72, 0.0, ()),
+    (9000, 9, 72, 2104, 1.0, (0, 8)),
+    (830, 2, 2904, 2904, 0.0, ()),
 ]
 IDS = ["-".join(str(v) for v in s[:4]) for s in SHAPES]
 
@@ -35,33 +45,36 @@ def _case(shape, seed=0):
 
 def _each(c, fn, shape):
     """fn(rows of each group, e) put together over the groups (rows outside them: 0)."""
-    ref, size = torch.zeros(shape, dtype=torch.float64), torch.zeros(shape, dtype=torch.float64)
+    ref = torch.zeros(shape, dtype=torch.float64, device=DEV)
+    size = torch.zeros(shape, dtype=torch.float64, device=DEV)
     for e in range(c["E"]):
         a, b = int(c["off"][e]), int(c["off"][e + 1])
         fn(e, slice(a, b), ref, size)
-    return ref, size
+    return ref.cpu(), size.cpu()
+
+
+def _wide(t):
+    return t.to(DEV).double()
 
 
 def _fwd(c):
     def one(e, s, ref, size):
-        w = c["w"][e].double().t()
-        ref[s] = c["x"][s].double() @ w
-        size[s] = c["x"][s].double().abs() @ w.abs()
+        x, w = _wide(c["x"][s]), _wide(c["w"][e]).t()
+        ref[s], size[s] = x @ w, x.abs() @ w.abs()
     return _each(c, one, (c["P"], c["N"]))
 
 
 def _dx(c):
     def one(e, s, ref, size):
-        w = c["w"][e].double()
-        ref[s] = c["dy"][s].double() @ w
-        size[s] = c["dy"][s].double().abs() @ w.abs()
+        dy, w = _wide(c["dy"][s]), _wide(c["w"][e])
+        ref[s], size[s] = dy @ w, dy.abs() @ w.abs()
     return _each(c, one, (c["P"], c["K"]))
 
 
 def _dw(c):
     def one(e, s, ref, size):
-        ref[e] = c["dy"][s].double().t() @ c["x"][s].double()
-        size[e] = c["dy"][s].double().abs().t() @ c["x"][s].double().abs()
+        dy, x = _wide(c["dy"][s]).t(), _wide(c["x"][s])
+        ref[e], size[e] = dy @ x, dy.abs() @ x.abs()
     return _each(c, one, (c["E"], c["N"], c["K"]))
 
 
@@ -114,11 +127,12 @@ def test_dw_accumulates(out):
     assert c["counts"][5] == 0 and torch.equal(dw[5].cpu(), old[5])
 
 
-@pytest.mark.parametrize("rows", [40, 300, 1100])
-def test_rows_outside_every_group(rows):
+@pytest.mark.parametrize("rows,N,K", [(40, 264, 136), (300, 264, 136), (1100, 264, 136), (11, 264, 136),
+                                      (2000, 2600, 136), (2000, 136, 2600)])
+def test_rows_outside_every_group(rows, N, K):
     """Groups that start after row 0 and end before row P: the other rows are neither read
     (NaN there changes nothing) nor written."""
-    P, E, N, K, lead = rows, 3, 264, 136, 3
+    P, E, lead = rows, 3, 3
     counts = split_counts(P - lead - 5, E, 1)
     off = offsets_of(counts, lead)
     g = gen(4)
@@ -138,11 +152,12 @@ def test_rows_outside_every_group(rows):
     within(moe.grouped_matmul_dw(*_d(c, "dy", "x", "off")), ref, product_bound(ref, size, max(counts), torch.bfloat16))
 
 
-@pytest.mark.parametrize("P", [60, 500])
-def test_nan_and_infinity_stay_in_their_rows(P):
+@pytest.mark.parametrize("P,N,K", [(14, 200, 136), (60, 200, 136), (500, 200, 136), (2500, 2200, 136),
+                                   (2500, 136, 2200), (2500, 1104, 1032)])
+def test_nan_and_infinity_stay_in_their_rows(P, N, K):
     """A NaN row and an infinite one change only what their formula reads: in y and dx their
     own rows, in dw their own group."""
-    c = _case((P, 4, 200, 136, 0.0, ()))
+    c = _case((P, 4, N, K, 0.0, ()))
     bad, inf = int(c["off"][1]), int(c["off"][2])  # first rows of groups 1 and 2
     for name in ("x", "dy"):
         c[name][bad] = float("nan")
@@ -182,7 +197,8 @@ def _act64(z, act):
             "gelu_tanh": lambda: 0.5 * z * (1 + torch.tanh((2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3)))}[act]()
 
 
-LINEAR = [(1, 8, 8), (1, 1032, 520), (3, 264, 136), (17, 72, 2056), (70, 128, 64), (300, 520, 264), (1030, 776, 520)]
+LINEAR = [(1, 8, 8), (1, 1032, 520), (3, 264, 136), (16, 72, 2056), (17, 72, 2056), (70, 128, 64), (300, 520, 264),
+          (1030, 776, 520), (1500, 1704, 136), (3000, 2104, 200)]
 
 
 @pytest.mark.parametrize("act", list(moe.ACTS))
@@ -246,11 +262,11 @@ def _all(c, b, r):
             moe.linear_dx(dy, w[1]), moe.linear_dw(dy, x, out_dtype=torch.float32)]
 
 
-@pytest.mark.parametrize("P", [12, 600])
-def test_two_streams_and_repeats_give_the_same_bits(P):
-    c = _case((P, 4, 264, 136, 0.5, ()))
+@pytest.mark.parametrize("P,N,K", [(12, 264, 136), (600, 264, 136), (2100, 2600, 264)])
+def test_two_streams_and_repeats_give_the_same_bits(P, N, K):
+    c = _case((P, 4, N, K, 0.5, ()))
     d = _d(c, "x", "w", "off", "dy")
-    b, r = torch.randn(264, device=DEV), bf16(gen(1), P, 264).to(DEV)
+    b, r = torch.randn(N, device=DEV), bf16(gen(1), P, N).to(DEV)
     first = _all(d, b, r)
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
@@ -265,10 +281,10 @@ def test_two_streams_and_repeats_give_the_same_bits(P):
                 assert torch.equal(a, e)
 
 
-@pytest.mark.parametrize("P", [12, 600])
-def test_graph_replays_equal_eager(P):
-    cases = [_case((P, 4, 264, 136, 0.5, ()), seed) for seed in range(3)]
-    b, r = torch.randn(264, device=DEV), bf16(gen(1), P, 264).to(DEV)
+@pytest.mark.parametrize("P,N,K", [(12, 264, 136), (600, 264, 136), (2100, 2600, 264)])
+def test_graph_replays_equal_eager(P, N, K):
+    cases = [_case((P, 4, N, K, 0.5, ()), seed) for seed in range(3)]
+    b, r = torch.randn(N, device=DEV), bf16(gen(1), P, N).to(DEV)
     bufs = _d(cases[0], "x", "w", "off", "dy")
     eager = []
     for c in cases:
