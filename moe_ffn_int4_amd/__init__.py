@@ -603,14 +603,22 @@ ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _OUT = (torch.bfloat16, torch.float32)
 
 
+# the current stream's handle without a Stream object: the object costs 1.8 us of the
+# 7 us that a small call takes on the host
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _run(fn, first: torch.Tensor, *args) -> None:
     """fn(*args, stream) with `first`'s device current."""
-    dev = first.device
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    index = first.device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != MOE_OK:
+        _check(status)
 
 
 def _same_device(first: torch.Tensor, *rest: Optional[torch.Tensor]) -> None:

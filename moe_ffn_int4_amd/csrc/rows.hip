@@ -92,8 +92,9 @@ __global__ __launch_bounds__(NT) void swiglu_backward_kernel(const uint16_t* __r
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float s = sigmoid_rn(g[i]);
-        const float slope = act_slope(g[i], MOE_ACT_SILU);
-        u[i] = d[i] * u[i] * slope;
+        // the bound as in act_slope
+        const float c = __builtin_amdgcn_fmed3f(g[i], -90.0f, 90.0f);
+        u[i] = d[i] * u[i] * fmaf(c * s, 1.0f - s, s);
         g[i] = d[i] * (g[i] * s);
     }
     save8(dz + r * 2 * h + c * 8, u);
@@ -120,29 +121,46 @@ hipError_t launch_swiglu_backward(const uint16_t* dy, const uint16_t* z, int64_t
 
 // A block takes `rows` rows from blockIdx.y * rows and up to 64 pieces of columns;
 // lanes (a power of two covering the columns, at most 64) walk the columns and the
-// block's other threads the rows. Each thread sums its rows, the block its threads
-// in order, and dz_finish the slices in order.
-__global__ __launch_bounds__(NT) void linear_dz_kernel(const uint16_t* dy, const uint16_t* z, int act,
-                                                       int64_t T, int64_t N, int shift, int64_t rows,
-                                                       uint16_t* dz, float* __restrict__ sums) {
+// block's other threads the rows, two at a time. Each thread sums its rows, the
+// block its threads in order, and dz_finish the slices in order. ACT is a template
+// argument: the switch would be taken for every value.
+template <int ACT>
+__global__ __launch_bounds__(NT) void linear_dz_kernel(const uint16_t* dy, const uint16_t* z, int64_t T,
+                                                       int64_t N, int shift, int64_t rows, uint16_t* dz,
+                                                       float* __restrict__ sums) {
     __shared__ float part[NT * 8];
     const int64_t c = (static_cast<int64_t>(blockIdx.x) << shift) + (threadIdx.x & ((1 << shift) - 1));
     const int first = threadIdx.x >> shift, stride = NT >> shift;
     const int64_t r0 = blockIdx.y * rows, r1 = r0 + rows < T ? r0 + rows : T;
     float sum[8] = {};
+    auto one = [&](float* d, const float* v, int64_t at) __attribute__((always_inline)) {
+        if (ACT != MOE_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] *= act_slope(v[i], ACT);
+            save8(dz + at, d);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += d[i];
+    };
     if (c * 8 < N) {
-        for (int64_t r = r0 + first; r < r1; r += stride) {
-            float d[8];
-            load8(dy + r * N + c * 8, d);
-            if (act != MOE_ACT_NONE) {
-                float v[8];
-                load8(z + r * N + c * 8, v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] *= act_slope(v[i], act);
-                save8(dz + r * N + c * 8, d);
+        const int64_t step = stride * N;
+        int64_t at = (r0 + first) * N + c * 8, r = r0 + first;
+        for (; r + stride < r1; r += 2 * stride, at += 2 * step) {
+            float d0[8], d1[8], v0[8], v1[8];
+            load8(dy + at, d0);
+            load8(dy + at + step, d1);
+            if (ACT != MOE_ACT_NONE) {
+                load8(z + at, v0);
+                load8(z + at + step, v1);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += d[i];
+            one(d0, v0, at);
+            one(d1, v1, at + step);
+        }
+        if (r < r1) {
+            float d0[8], v0[8];
+            load8(dy + at, d0);
+            if (ACT != MOE_ACT_NONE) load8(z + at, v0);
+            one(d0, v0, at);
         }
     }
     if (!sums) return;
@@ -160,16 +178,26 @@ __global__ __launch_bounds__(NT) void linear_dz_kernel(const uint16_t* dy, const
     }
 }
 
-__global__ __launch_bounds__(NT) void dz_finish_kernel(const float* __restrict__ partial, int64_t slices,
-                                                       int64_t N, float* __restrict__ db) {
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x;
-    if (c >= N) return;
+// A block adds the slices of 32 columns: eight threads a column take every eighth slice,
+// and their sums are added in order. (One thread a column: 128 loads in a row.)
+__global__ __launch_bounds__(NT) void dz_finish_kernel(const float* __restrict__ partial, int slices, int64_t N,
+                                                       float* __restrict__ db) {
+    __shared__ float part[NT];
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
     float s = 0.f;
-    for (int64_t i = 0; i < slices; ++i) s += partial[i * N + c];
+    if (c < N) {
+#pragma unroll 8
+        for (int i = threadIdx.x >> 5; i < slices; i += 8) s += partial[i * N + c];
+    }
+    part[threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.x >= 32 || c >= N) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += part[i * 32 + threadIdx.x];
     db[c] = s;
 }
 
-constexpr int64_t kDzRows = 128;
+constexpr int64_t kDzRows = 64;
 constexpr int64_t kDzMaxSlices = 1024;
 
 int64_t linear_dz_slices(int64_t T, int64_t N) {
@@ -185,12 +213,17 @@ hipError_t launch_linear_dz(const uint16_t* dy, const uint16_t* z, int act, int6
     while ((1 << shift) < 64 && (8 << shift) < N) ++shift;
     const int64_t cols = (N + (8 << shift) - 1) >> (shift + 3);
     float* sums = !db ? nullptr : slices == 1 ? db : partial;
-    hipLaunchKernelGGL(linear_dz_kernel, dim3(static_cast<unsigned>(cols), static_cast<unsigned>(slices)),
-                       dim3(NT), 0, stream, dy, z, act, T, N, shift, rows, dz, sums);
+    auto* kernel = act == MOE_ACT_RELU        ? linear_dz_kernel<MOE_ACT_RELU>
+                   : act == MOE_ACT_SILU      ? linear_dz_kernel<MOE_ACT_SILU>
+                   : act == MOE_ACT_GELU      ? linear_dz_kernel<MOE_ACT_GELU>
+                   : act == MOE_ACT_GELU_TANH ? linear_dz_kernel<MOE_ACT_GELU_TANH>
+                                              : linear_dz_kernel<MOE_ACT_NONE>;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(cols), static_cast<unsigned>(slices)), dim3(NT), 0,
+                       stream, dy, z, T, N, shift, rows, dz, sums);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !db || slices == 1) return e;
-    hipLaunchKernelGGL(dz_finish_kernel, dim3(static_cast<unsigned>((N + NT - 1) / NT)), dim3(NT), 0, stream,
-                       partial, slices, N, db);
+    hipLaunchKernelGGL(dz_finish_kernel, dim3(static_cast<unsigned>((N + 31) / 32)), dim3(NT), 0, stream,
+                       partial, static_cast<int>(slices), N, db);
     return hipGetLastError();
 }
 
