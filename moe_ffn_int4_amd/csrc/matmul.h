@@ -410,6 +410,64 @@ __device__ __forceinline__ void store8(const MatmulArgs& a, int64_t row, int64_t
     }
 }
 
+// Rows of the output start on 128-byte lines, so that stores of whole tiles write whole lines.
+__device__ __forceinline__ bool whole_lines(const MatmulArgs& a, int64_t ld) {
+    return ((reinterpret_cast<uintptr_t>(a.out) | static_cast<uintptr_t>(ld * (a.out_fp32 ? 4 : 2))) & 127) == 0;
+}
+
+// The products' own results, 16 rows x 32 JJ columns at (row0, col0) of the tile
+// whose rows and columns end at `rows` and `cols`: acc[2 h], acc[2 h + 1] are the
+// sub-tiles of columns 32 h. Lanes l and l ^ 8 exchange halves, so that a store
+// instruction covers whole 128-byte lines: 8 rows of 64 bf16 or 32 fp32 values. STREAM:
+// the lines are not kept in L2 (a weight gradient is read much later, and its lines
+// push the operands out).
+template <int JJ, bool STREAM>
+__device__ __forceinline__ void store_rows(const MatmulArgs& a, const f32x4* acc, int64_t out_row, int64_t ld,
+                                           int64_t out_col, int row0, int rows, int col0, int cols, int lane) {
+    const int i16 = lane & 15, q = lane >> 4;
+    const bool low = i16 < 8;
+    // the value of lane l ^ 8 (a rotation by 8 in each row of 16 lanes)
+    auto other = [](uint32_t v) {
+        return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x128, 0xf, 0xf, true));
+    };
+    // store A: rows 0..7, store B: rows 8..15; low lanes the first half line, high lanes the second
+    const int ra = row0 + (i16 & 7), rb = ra + 8;
+    const int size = a.out_fp32 ? 4 : 2;
+    auto put = [&](const u32x4& first, const u32x4& second, int col, int half, int width) __attribute__((always_inline)) {
+        u32x4 got;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) got[k] = other(low ? second[k] : first[k]);
+        const u32x4 va = low ? first : got, vb = low ? got : second;
+        const int c = col + (low ? 0 : half);
+        if (c + width > cols) return;
+        uint8_t* o = static_cast<uint8_t*>(a.out) + ((out_row + ra) * ld + out_col + c) * size;
+        u32x4* const pa = reinterpret_cast<u32x4*>(o);
+        u32x4* const pb = reinterpret_cast<u32x4*>(o + 8 * ld * size);
+        if (ra < rows) {
+            if (STREAM) __builtin_nontemporal_store(va, pa);
+            else *pa = va;
+        }
+        if (rb < rows) {
+            if (STREAM) __builtin_nontemporal_store(vb, pb);
+            else *pb = vb;
+        }
+    };
+    if (a.out_fp32) {
+#pragma unroll
+        for (int h = 0; h < JJ; ++h)
+            put(__builtin_bit_cast(u32x4, acc[2 * h]), __builtin_bit_cast(u32x4, acc[2 * h + 1]),
+                col0 + 32 * h + 4 * q, 16, 4);
+    } else {
+#pragma unroll
+        for (int h = 0; h + 1 < JJ; h += 2) {
+            float v[8], w[8];
+            eight_columns(acc[2 * h], acc[2 * h + 1], v);
+            eight_columns(acc[2 * h + 2], acc[2 * h + 3], w);
+            put(pack8(v), pack8(w), col0 + 32 * h + eight_columns_at(q), 32, 8);
+        }
+    }
+}
+
 // The same for one value.
 template <bool LINEAR>
 __device__ __forceinline__ void store1(const MatmulArgs& a, int64_t row, int64_t ld, int64_t col, float v) {

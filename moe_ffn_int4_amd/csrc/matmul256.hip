@@ -49,21 +49,28 @@ __device__ __forceinline__ void block_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// The tiles of this block's XCD, group by group. XCDs share every group: XCD x takes
-// the contiguous eighth (x + e) % 8 of group e's tiles of 256 rows (walked in bands
-// of kBand rows), then the same eighth of its last row of tiles where that has at
-// most 128 rows, which cost about half. So every XCD has nearly the same work
-// whatever the group sizes, a group's weights are read by one XCD at a time, and
-// equal tiles stand together for the blocks' round robin.
+// The tiles of this block's XCD, group by group: of each group some of its tiles of 256
+// rows, walked in bands of up to kBand rows, then some of its last row of tiles where
+// that has at most 128 rows.
+//
+// XCDs share every group: XCD x takes the contiguous eighth (x + e) % 8 of group e's
+// tiles of each kind, so that every XCD has the same work whatever the group sizes (a
+// line of all groups' tiles cut by estimated cost: 16 experts, 8192 rows, 16384 x 5120,
+// forward 1406 against 1305 us, dx 1428 against 1405). Groups of few tiles would leave
+// an XCD one or two of each, with little to share in its L2; their tiles stand in one
+// line, of which each XCD takes an eighth: 32 experts of 128 rows, 4096 x 4096 (16 tiles
+// each), 224 against 266 us.
 struct Group {
     int before, tiles;  // tiles of earlier groups, and of this one, on this XCD
+    int whole, start;   // of these, tiles of 256 rows, from the group's tile `start`;
+    int column;         // the rest are the small ones from this column
     int first, count;   // rows
 };
 constexpr int kTable = kMaxExperts * static_cast<int>(sizeof(Group));
+constexpr uint32_t kFewTiles = 32;
 
-// first tile of eighth x of n (n * 8 fits: the host refuses more than 2^27 tiles)
-__device__ __forceinline__ uint32_t eighth(uint32_t n, int x) { return n * x >> 3; }
-__device__ __forceinline__ int share(uint32_t n, int x) { return static_cast<int>(eighth(n, x + 1) - eighth(n, x)); }
+// first of eighth x of n (the host refuses more than 2^26 tiles)
+__device__ __forceinline__ int eighth(uint32_t n, int x) { return static_cast<int>((n >> 3) * x + ((n & 7) * x >> 3)); }
 
 // tiles of BM rows, and whether a smaller one follows them
 template <int MODE>
@@ -77,41 +84,74 @@ __device__ __forceinline__ void row_tiles(const MatmulArgs& a, int count, int& w
     }
 }
 
+__device__ __forceinline__ uint32_t inclusive_scan(uint32_t v, int lane) {
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const uint32_t u = __shfl_up(v, off, kWave);
+        if (lane >= off) v += u;
+    }
+    return v;
+}
+
 // Fills the table (every wave the same values) and returns the number of tiles.
 template <int MODE>
 __device__ __forceinline__ int fill_table(const MatmulArgs& a, Group* table, int ncol, int lane) {
     const int xcd = blockIdx.x & 7;
     Group g[4];
-    int sum = 0;
+    int whole[4], small[4];
+    uint32_t mine = 0, groups = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int e = 4 * lane + i;
-        g[i] = Group{0, 0, 0, 0};
+        g[i] = Group{0, 0, 0, 0, 0, 0, 0};
+        whole[i] = small[i] = 0;
         if (e < a.E) {
             int64_t first;
             group_rows(a, e, first, g[i].count);
             g[i].first = static_cast<int>(first);
-            int whole, small;
-            row_tiles<MODE>(a, g[i].count, whole, small);
-            const int x = (xcd + e) & 7;
-            g[i].tiles = share(whole * ncol, x) + (small ? share(ncol, x) : 0);
-            if (MODE == kDw && a.accumulate && g[i].count == 0) g[i].tiles = 0;
+            int w, s;
+            row_tiles<MODE>(a, g[i].count, w, s);
+            whole[i] = w * ncol;
+            small[i] = s * ncol;
+            if (MODE == kDw && a.accumulate && g[i].count == 0) whole[i] = 0;
         }
-        g[i].before = sum;
-        sum += g[i].tiles;
+        mine += whole[i] + small[i];
+        groups += whole[i] + small[i] > 0;
     }
-    int incl = sum;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int v = __shfl_up(incl, off, kWave);
-        if (lane >= off) incl += v;
-    }
+    const uint32_t upto = inclusive_scan(mine, lane);
+    const uint32_t all = __builtin_amdgcn_readlane(upto, 63);
+    groups = inclusive_scan(groups, lane);
+    const bool line = all < kFewTiles * __builtin_amdgcn_readlane(groups, 63);
+    const int lo = eighth(all, xcd), hi = eighth(all, xcd + 1);
+    int at = static_cast<int>(upto - mine);  // of the first of these four groups in the line
+    uint32_t sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        g[i].before += incl - sum;
+        const int n = whole[i] + small[i], x = (xcd + 4 * lane + i) & 7;
+        if (line) {
+            const int from = lo <= at ? 0 : lo < at + n ? lo - at : n;
+            const int to = hi <= at ? 0 : hi < at + n ? hi - at : n;
+            g[i].start = from < whole[i] ? from : whole[i];
+            g[i].whole = (to < whole[i] ? to : whole[i]) - g[i].start;
+            g[i].column = from < whole[i] ? 0 : from - whole[i];
+            g[i].tiles = to - from;
+        } else {
+            g[i].start = eighth(whole[i], x);
+            g[i].whole = eighth(whole[i], x + 1) - g[i].start;
+            g[i].column = eighth(small[i], x);
+            g[i].tiles = g[i].whole + eighth(small[i], x + 1) - g[i].column;
+        }
+        at += n;
+        g[i].before = static_cast<int>(sum);
+        sum += g[i].tiles;
+    }
+    const uint32_t incl = inclusive_scan(sum, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        g[i].before += static_cast<int>(incl - sum);
         table[4 * lane + i] = g[i];
     }
-    return __builtin_amdgcn_readlane(incl, 63);
+    return static_cast<int>(__builtin_amdgcn_readlane(incl, 63));
 }
 
 // The tile at `slot` of this XCD's list of `total`. If the last round of 32 (one a
@@ -141,27 +181,26 @@ __device__ __forceinline__ bool find(const MatmulArgs& a, const Group* table, in
     }
     const int src = __builtin_amdgcn_readfirstlane(
         __ffsll(static_cast<unsigned long long>(__ballot(e >= 0))) - 1);
-    e = __builtin_amdgcn_readlane(e, src);
+    t.group = __builtin_amdgcn_readlane(e, src);
     slot -= __builtin_amdgcn_readlane(g.before, src);
-    t.group = e;
+    const int mine = __builtin_amdgcn_readlane(g.whole, src);
     int first = __builtin_amdgcn_readlane(g.first, src);
     t.nrows = __builtin_amdgcn_readlane(g.count, src);
     int whole, small;
     row_tiles<MODE>(a, t.nrows, whole, small);
-    const int x = ((blockIdx.x & 7) + e) & 7;
-    const uint32_t n = whole * ncol;
-    const int mine = share(n, x);
     if (slot < mine) {
-        // bands of kBand row tiles, column by column
-        const uint32_t lin = eighth(n, x) + slot, span = kBand * ncol;
+        // bands of equal height, at most kBand row tiles, column by column
+        const uint32_t lin = slot + __builtin_amdgcn_readlane(g.start, src);
+        const uint32_t bands = (static_cast<uint32_t>(whole) + kBand - 1) / kBand;
+        const uint32_t height = (whole + bands - 1) / bands, span = height * ncol;
         const uint32_t band = lin / span, within = lin - band * span;
-        const uint32_t left = whole - band * kBand, here = left < kBand ? left : kBand;
+        const uint32_t left = whole - band * height, here = left < height ? left : height;
         const uint32_t col = within / here;
-        rt = __builtin_amdgcn_readfirstlane(static_cast<int>(band * kBand + within - col * here));
+        rt = __builtin_amdgcn_readfirstlane(static_cast<int>(band * height + within - col * here));
         ct = __builtin_amdgcn_readfirstlane(static_cast<int>(col));
     } else {
         rt = whole;
-        ct = static_cast<int>(eighth(ncol, x)) + slot - mine;
+        ct = slot - mine + __builtin_amdgcn_readlane(g.column, src);
     }
     if (MODE != kDw) {
         first += rt * BM;
@@ -385,6 +424,7 @@ __device__ __forceinline__ void run_tile(const MatmulArgs& a, const Work<MODE>& 
     // all waves have read all of LDS
     const int rows = w.rows, cols = w.cols, col0 = w.col0;
     const int64_t out_row = w.out_row, ldo = MODE == kFwd ? a.N : a.K;
+    const bool stream = MODE == kDw && whole_lines(a, ldo);
     next();
 
     // opaque, so that the addresses are not computed once for all tiles and kept
@@ -393,7 +433,13 @@ __device__ __forceinline__ void run_tile(const MatmulArgs& a, const Work<MODE>& 
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
         if ((SMALL || i >= 4) && (i & 3) > 0 && (i & 3) >= subs) continue;
-        const int row = (SMALL ? wm * each : i < 4 ? wm * 64 : 128 + wm * each) + 16 * (i & 3) + i16;
+        const int row0 = (SMALL ? wm * each : i < 4 ? wm * 64 : 128 + wm * each) + 16 * (i & 3);
+        if (!LINEAR && !a.accumulate) {
+            if (stream) store_rows<2, true>(a, acc[i], out_row, ldo, col0, row0, rows, wn * 64, cols, lane);
+            else store_rows<2, false>(a, acc[i], out_row, ldo, col0, row0, rows, wn * 64, cols, lane);
+            continue;
+        }
+        const int row = row0 + i16;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float v[8];
@@ -455,10 +501,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul256_kernel(MatmulArgs a)
 template <int MODE>
 static int64_t matmul256_blocks(const MatmulArgs& a) {
     const int64_t ncol = ((MODE == kFwd ? a.N : a.K) + BN - 1) / BN;
+    if (MODE == kDw) {
+        // each group's eighth rounds up by less than a tile; cut tiles
+        return 8 * (a.E * ((a.N + BM - 1) / BM * ncol / 8 + 1) + kXcdCus / 2);
+    }
+    // an XCD's shares of a group's two kinds round up by less than a tile each; cut tiles
     const int64_t groups = a.E < a.P ? a.E : a.P;
-    const int64_t rows = MODE == kDw ? a.E * ((a.N + BM - 1) / BM) : a.P / BM + groups;
-    // an XCD's shares round up by less than one tile for each group and kind; cut tiles
-    return 8 * (rows * ncol / 8 + 2 * groups + 1 + kXcdCus / 2);
+    return 8 * ((a.P / BM + groups) * ncol / 8 + 2 * groups + 1 + kXcdCus / 2);
 }
 
 template <int MODE, bool LINEAR>

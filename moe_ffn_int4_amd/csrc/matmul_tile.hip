@@ -90,6 +90,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_tile_kernel(MatmulArgs 
     const int i16 = lane & 15, q = lane >> 4;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
+        if (!LINEAR && !a.accumulate && (S > 2 || a.out_fp32)) {
+            if (MODE == kDw && whole_lines(a, o.ldo))
+                store_rows<S / 2, true>(a, acc[i], o.out_row, o.ldo, o.col0, wm + 16 * i, o.rows, wn, o.cols, lane);
+            else
+                store_rows<S / 2, false>(a, acc[i], o.out_row, o.ldo, o.col0, wm + 16 * i, o.rows, wn, o.cols, lane);
+            continue;
+        }
         const int row = wm + 16 * i + i16;
 #pragma unroll
         for (int h = 0; h < S / 2; ++h) {
