@@ -361,114 +361,234 @@ __device__ __forceinline__ void eight_columns(f32x4 x, f32x4 y, float* v) {
 }
 __device__ __forceinline__ int eight_columns_at(int q) { return 16 * (q & 1) + 8 * (q >> 1); }
 
-// Eight consecutive values of output row `row` (index into the whole output),
-// columns col .. col + 7: bias, activation and residual (LINEAR), the old value
-// (accumulate), one rounding, one or two 16-byte stores.
-template <bool LINEAR>
-__device__ __forceinline__ void store8(const MatmulArgs& a, int64_t row, int64_t ld, int64_t col, float* v) {
-    const int64_t at = row * ld + col;
-    if (LINEAR) {
-        if (a.bias) {
-            const f32x4 b0 = *reinterpret_cast<const f32x4*>(a.bias + col);
-            const f32x4 b1 = *reinterpret_cast<const f32x4*>(a.bias + col + 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] += b0[i];
-                v[4 + i] += b1[i];
-            }
-        }
-        if (a.z) *reinterpret_cast<u32x4*>(a.z + at) = pack8(v);
-        if (a.act != 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], a.act);
-        }
-        if (a.residual) {
-            float r[8];
-            unpack8(*reinterpret_cast<const u32x4*>(a.residual + at), r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += r[i];
-        }
-    }
-    if (a.out_fp32) {
-        float* o = static_cast<float*>(a.out) + at;
-        f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
-        if (a.accumulate) {
-            lo += *reinterpret_cast<const f32x4*>(o);
-            hi += *reinterpret_cast<const f32x4*>(o + 4);
-        }
-        *reinterpret_cast<f32x4*>(o) = lo;
-        *reinterpret_cast<f32x4*>(o + 4) = hi;
-    } else {
-        uint16_t* o = static_cast<uint16_t*>(a.out) + at;
-        if (a.accumulate) {
-            float old[8];
-            unpack8(*reinterpret_cast<const u32x4*>(o), old);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += old[i];
-        }
-        *reinterpret_cast<u32x4*>(o) = pack8(v);
-    }
-}
-
 // Rows of the output start on 128-byte lines, so that stores of whole tiles write whole lines.
 __device__ __forceinline__ bool whole_lines(const MatmulArgs& a, int64_t ld) {
     return ((reinterpret_cast<uintptr_t>(a.out) | static_cast<uintptr_t>(ld * (a.out_fp32 ? 4 : 2))) & 127) == 0;
 }
 
-// The products' own results, 16 rows x 32 JJ columns at (row0, col0) of the tile
-// whose rows and columns end at `rows` and `cols`: acc[2 h], acc[2 h + 1] are the
-// sub-tiles of columns 32 h. Lanes l and l ^ 8 exchange halves, so that a store
-// instruction covers whole 128-byte lines: 8 rows of 64 bf16 or 32 fp32 values. STREAM:
-// the lines are not kept in L2 (a weight gradient is read much later, and its lines
-// push the operands out).
-template <int JJ, bool STREAM>
-__device__ __forceinline__ void store_rows(const MatmulArgs& a, const f32x4* acc, int64_t out_row, int64_t ld,
-                                           int64_t out_col, int row0, int rows, int col0, int cols, int lane) {
+// Where a wave's accumulators go: 16 rows from row0(i) for sub-tile row i, 32 columns from
+// col0 for each pair of sub-tiles; rows and columns of the tile end at rows and cols,
+// which stands at out_row, out_col of the output.
+struct Place {
+    int64_t out_row, ld, out_col;
+    int rows, col0, cols;
+};
+
+// The products' own results of NI x 16 rows, 32 JJ columns. Lanes l and l ^ 8 exchange
+// halves, so that a store instruction covers whole 128-byte lines: 8 rows of 64 bf16
+// or 32 fp32 values. (Without: 64-byte pieces. 128 x 1000 x 712 weight gradients in
+// fp32 116 us, 95 with.) STREAM: the lines are not kept in L2; a weight gradient is read
+// much later, and its lines would push the operands out (32 x 4096 x 4096: 360 us, 306
+// with), but parts of lines must meet there. ACC: added to the old values, which are
+// loaded for two sub-tile rows at once.
+template <int NI, int JJ, bool STREAM, bool ACC, typename Row>
+__device__ __forceinline__ void store_rows(const MatmulArgs& a, const f32x4 (*acc)[2 * JJ], const Place& at,
+                                           Row&& row0, int lane) {
     const int i16 = lane & 15, q = lane >> 4;
     const bool low = i16 < 8;
+    const int size = a.out_fp32 ? 4 : 2;
     // the value of lane l ^ 8 (a rotation by 8 in each row of 16 lanes)
     auto other = [](uint32_t v) {
         return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x128, 0xf, 0xf, true));
     };
-    // store A: rows 0..7, store B: rows 8..15; low lanes the first half line, high lanes the second
-    const int ra = row0 + (i16 & 7), rb = ra + 8;
-    const int size = a.out_fp32 ? 4 : 2;
-    auto put = [&](const u32x4& first, const u32x4& second, int col, int half, int width) __attribute__((always_inline)) {
-        u32x4 got;
+    constexpr int BATCH = ACC ? 2 : 1;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) got[k] = other(low ? second[k] : first[k]);
-        const u32x4 va = low ? first : got, vb = low ? got : second;
-        const int c = col + (low ? 0 : half);
-        if (c + width > cols) return;
-        uint8_t* o = static_cast<uint8_t*>(a.out) + ((out_row + ra) * ld + out_col + c) * size;
-        u32x4* const pa = reinterpret_cast<u32x4*>(o);
-        u32x4* const pb = reinterpret_cast<u32x4*>(o + 8 * ld * size);
-        if (ra < rows) {
-            if (STREAM) __builtin_nontemporal_store(va, pa);
-            else *pa = va;
-        }
-        if (rb < rows) {
-            if (STREAM) __builtin_nontemporal_store(vb, pb);
-            else *pb = vb;
-        }
-    };
-    if (a.out_fp32) {
+    for (int i0 = 0; i0 < NI; i0 += BATCH) {
+        u32x4 v[BATCH][JJ][2];
+        uint8_t* p[BATCH][JJ][2];
+        bool ok[BATCH][JJ][2];
 #pragma unroll
-        for (int h = 0; h < JJ; ++h)
-            put(__builtin_bit_cast(u32x4, acc[2 * h]), __builtin_bit_cast(u32x4, acc[2 * h + 1]),
-                col0 + 32 * h + 4 * q, 16, 4);
-    } else {
+        for (int b = 0; b < BATCH; ++b) {
+            const int row = row0(i0 + b);  // negative: none
+            // first: rows 0..7, second: 8..15; low lanes the first half line, high lanes the second
+            auto put = [&](int n, const u32x4& first, const u32x4& second, int col, int half, int width)
+                           __attribute__((always_inline)) {
+                u32x4 got;
 #pragma unroll
-        for (int h = 0; h + 1 < JJ; h += 2) {
-            float v[8], w[8];
-            eight_columns(acc[2 * h], acc[2 * h + 1], v);
-            eight_columns(acc[2 * h + 2], acc[2 * h + 3], w);
-            put(pack8(v), pack8(w), col0 + 32 * h + eight_columns_at(q), 32, 8);
+                for (int k = 0; k < 4; ++k) got[k] = other(low ? second[k] : first[k]);
+                v[b][n][0] = low ? first : got;
+                v[b][n][1] = low ? got : second;
+                const int c = col + (low ? 0 : half), r = row + (i16 & 7);
+                p[b][n][0] = static_cast<uint8_t*>(a.out) + ((at.out_row + r) * at.ld + at.out_col + c) * size;
+                p[b][n][1] = p[b][n][0] + 8 * at.ld * size;
+                ok[b][n][0] = row >= 0 && r < at.rows && c + width <= at.cols;
+                ok[b][n][1] = row >= 0 && r + 8 < at.rows && c + width <= at.cols;
+            };
+            const f32x4* x = acc[i0 + b];
+            if (a.out_fp32) {
+#pragma unroll
+                for (int h = 0; h < JJ; ++h)
+                    put(h, __builtin_bit_cast(u32x4, x[2 * h]), __builtin_bit_cast(u32x4, x[2 * h + 1]),
+                        at.col0 + 32 * h + 4 * q, 16, 4);
+            } else {
+#pragma unroll
+                for (int h = 0; h < JJ; h += 2) {
+                    float lo[8], hi[8];
+                    eight_columns(x[2 * h], x[2 * h + 1], lo);
+                    if (JJ > 1) eight_columns(x[JJ > 1 ? 2 * h + 2 : 0], x[JJ > 1 ? 2 * h + 3 : 0], hi);
+                    if (JJ > 1) {
+                        put(h, pack8(lo), pack8(hi), at.col0 + 32 * h + eight_columns_at(q), 32, 8);
+                        ok[b][h + JJ / 2][0] = ok[b][h + JJ / 2][1] = false;
+                    } else {
+                        // 32 columns: no second half line to exchange
+                        const int c = at.col0 + eight_columns_at(q), r = row + i16;
+                        v[b][0][0] = pack8(lo);
+                        p[b][0][0] = static_cast<uint8_t*>(a.out) + ((at.out_row + r) * at.ld + at.out_col + c) * size;
+                        ok[b][0][0] = row >= 0 && r < at.rows && c + 8 <= at.cols;
+                        ok[b][0][1] = false;
+                    }
+                }
+            }
         }
+        if (ACC) {
+            u32x4 old[BATCH][JJ][2];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+                for (int n = 0; n < JJ; ++n)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (ok[b][n][k]) old[b][n][k] = *reinterpret_cast<const u32x4*>(p[b][n][k]);
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+                for (int n = 0; n < JJ; ++n)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (!ok[b][n][k]) continue;
+                        v[b][n][k] = __builtin_bit_cast(
+                            u32x4, __builtin_bit_cast(f32x4, v[b][n][k]) + __builtin_bit_cast(f32x4, old[b][n][k]));
+                    }
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+            for (int n = 0; n < JJ; ++n)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (!ok[b][n][k]) continue;
+                    u32x4* to = reinterpret_cast<u32x4*>(p[b][n][k]);
+                    if (STREAM) __builtin_nontemporal_store(v[b][n][k], to);
+                    else *to = v[b][n][k];
+                }
     }
 }
 
-// The same for one value.
+// Results with something to be added or applied: for linear, bias, activation and
+// residual; else the old values (accumulate). One rounding at the end. The bias is
+// loaded once, the residual or old values for two sub-tile rows at once before any
+// is stored: one at a time, each would wait for its own load (14203 x 4568 x 488 with
+// bias, gelu and residual: 178 us, 158 with).
+// ACT is a template argument: the switch would be taken, and its code repeated, for every
+// value.
+template <bool LINEAR, int ACT, int NI, int JJ, typename Row>
+__device__ __forceinline__ void store_applied(const MatmulArgs& a, const f32x4 (*acc)[2 * JJ], const Place& at,
+                                              Row&& row0, int lane) {
+    const int i16 = lane & 15, q = lane >> 4;
+    constexpr int BATCH = 2;
+    float bias[JJ][8];
+#pragma unroll
+    for (int h = 0; h < JJ; ++h) {
+        const int c = at.col0 + 32 * h + eight_columns_at(q);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) bias[h][k] = 0.f;
+        if (LINEAR && a.bias && c < at.cols) {
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(a.bias + at.out_col + c);
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(a.bias + at.out_col + c + 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bias[h][k] = lo[k];
+                bias[h][4 + k] = hi[k];
+            }
+        }
+    }
+    const uint16_t* add16 = LINEAR ? a.residual
+                                   : !a.out_fp32 ? static_cast<const uint16_t*>(a.out) : nullptr;
+    const float* add32 = !LINEAR && a.out_fp32 ? static_cast<const float*>(a.out) : nullptr;
+#pragma unroll
+    for (int i0 = 0; i0 < NI; i0 += BATCH) {
+        u32x4 old[BATCH][JJ][LINEAR ? 1 : 2];
+        bool ok[BATCH][JJ];
+        int64_t pos[BATCH][JJ];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int r0 = row0(i0 + b), r = r0 + i16;
+#pragma unroll
+            for (int h = 0; h < JJ; ++h) {
+                const int c = at.col0 + 32 * h + eight_columns_at(q);
+                ok[b][h] = r0 >= 0 && r < at.rows && c < at.cols;
+                pos[b][h] = (at.out_row + r) * at.ld + at.out_col + c;
+                if (!ok[b][h]) continue;
+                if (add16) old[b][h][0] = *reinterpret_cast<const u32x4*>(add16 + pos[b][h]);
+                if (!LINEAR && add32) {
+                    old[b][h][0] = *reinterpret_cast<const u32x4*>(add32 + pos[b][h]);
+                    old[b][h][LINEAR ? 0 : 1] = *reinterpret_cast<const u32x4*>(add32 + pos[b][h] + 4);
+                }
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+            for (int h = 0; h < JJ; ++h) {
+                float v[8];
+                eight_columns(acc[i0 + b][2 * h], acc[i0 + b][2 * h + 1], v);
+                if (!ok[b][h]) continue;
+                if (LINEAR) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] += bias[h][k];
+                    if (a.z) *reinterpret_cast<u32x4*>(a.z + pos[b][h]) = pack8(v);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], ACT);
+                }
+                if (add16) {
+                    float r[8];
+                    unpack8(old[b][h][0], r);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] += r[k];
+                }
+                if (!LINEAR && add32) {
+                    const f32x4 lo = __builtin_bit_cast(f32x4, old[b][h][0]);
+                    const f32x4 hi = __builtin_bit_cast(f32x4, old[b][h][LINEAR ? 0 : 1]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        v[k] += lo[k];
+                        v[4 + k] += hi[k];
+                    }
+                }
+                if (a.out_fp32) {
+                    float* o = static_cast<float*>(a.out) + pos[b][h];
+                    *reinterpret_cast<f32x4*>(o) = f32x4{v[0], v[1], v[2], v[3]};
+                    *reinterpret_cast<f32x4*>(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
+                } else {
+                    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + pos[b][h]) = pack8(v);
+                }
+            }
+    }
+}
+
+// All of a wave's results.
+template <int MODE, bool LINEAR, int NI, int JJ, typename Row>
+__device__ __forceinline__ void store_all(const MatmulArgs& a, const f32x4 (*acc)[2 * JJ], const Place& at,
+                                          Row&& row0, int lane) {
+    if (LINEAR && (a.bias || a.z || a.residual || a.act != MOE_ACT_NONE)) {
+        switch (a.act) {
+            case MOE_ACT_RELU: return store_applied<true, MOE_ACT_RELU, NI, JJ>(a, acc, at, row0, lane);
+            case MOE_ACT_SILU: return store_applied<true, MOE_ACT_SILU, NI, JJ>(a, acc, at, row0, lane);
+            case MOE_ACT_GELU: return store_applied<true, MOE_ACT_GELU, NI, JJ>(a, acc, at, row0, lane);
+            case MOE_ACT_GELU_TANH: return store_applied<true, MOE_ACT_GELU_TANH, NI, JJ>(a, acc, at, row0, lane);
+            default: return store_applied<true, MOE_ACT_NONE, NI, JJ>(a, acc, at, row0, lane);
+        }
+    } else if (MODE == kDw && a.accumulate) {
+        if (a.out_fp32) store_rows<NI, JJ, false, true>(a, acc, at, row0, lane);
+        else store_applied<false, MOE_ACT_NONE, NI, JJ>(a, acc, at, row0, lane);
+    } else if (MODE == kDw && whole_lines(a, at.ld)) {
+        store_rows<NI, JJ, true, false>(a, acc, at, row0, lane);
+    } else {
+        store_rows<NI, JJ, false, false>(a, acc, at, row0, lane);
+    }
+}
+
+// One value of a linear layer or product.
 template <bool LINEAR>
 __device__ __forceinline__ void store1(const MatmulArgs& a, int64_t row, int64_t ld, int64_t col, float v) {
     const int64_t at = row * ld + col;

@@ -364,10 +364,14 @@ __device__ __forceinline__ void run_tile(const MatmulArgs& a, const Work<MODE>& 
         for (int i = 0; i < 4; ++i) {
             if (i > 0 && i >= subs) continue;
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < 2; ++s) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     acc[4 * ih + i][j] = mfma_bf16(fb[j][s], fa[i][s], acc[4 * ih + i][j]);
+                // in this order: the two products of one accumulator stay four apart (the
+                // scheduler put them side by side in some builds, 13 % slower)
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         __builtin_amdgcn_s_setprio(0);
         block_barrier();
@@ -424,30 +428,17 @@ __device__ __forceinline__ void run_tile(const MatmulArgs& a, const Work<MODE>& 
     // all waves have read all of LDS
     const int rows = w.rows, cols = w.cols, col0 = w.col0;
     const int64_t out_row = w.out_row, ldo = MODE == kFwd ? a.N : a.K;
-    const bool stream = MODE == kDw && whole_lines(a, ldo);
     next();
 
     // opaque, so that the addresses are not computed once for all tiles and kept
     asm volatile("" : "+v"(lane));
-    const int i16 = lane & 15, q = lane >> 4;
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        if ((SMALL || i >= 4) && (i & 3) > 0 && (i & 3) >= subs) continue;
-        const int row0 = (SMALL ? wm * each : i < 4 ? wm * 64 : 128 + wm * each) + 16 * (i & 3);
-        if (!LINEAR && !a.accumulate) {
-            if (stream) store_rows<2, true>(a, acc[i], out_row, ldo, col0, row0, rows, wn * 64, cols, lane);
-            else store_rows<2, false>(a, acc[i], out_row, ldo, col0, row0, rows, wn * 64, cols, lane);
-            continue;
-        }
-        const int row = row0 + i16;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v[8];
-            eight_columns(acc[i][2 * h], acc[i][2 * h + 1], v);
-            const int col = wn * 64 + 32 * h + eight_columns_at(q);
-            if (row < rows && col < cols) store8<LINEAR>(a, out_row + row, ldo, col0 + col, v);
-        }
-    }
+    store_all<MODE, LINEAR, MI, 2>(
+        a, acc, Place{out_row, ldo, col0, rows, wn * 64, cols},
+        [&](int i) {
+            if ((SMALL || i >= 4) && (i & 3) > 0 && (i & 3) >= subs) return -1000000;
+            return (SMALL ? wm * each : i < 4 ? wm * 64 : 128 + wm * each) + 16 * (i & 3);
+        },
+        lane);
 }
 
 // Blocks walk their XCD's tiles in a round robin; a block requests its next tile's

@@ -32,6 +32,14 @@ struct StreamShape {
     static constexpr int kPieces = kSeg / 16;
 };
 
+// Chunks a wave's ring holds: a short reduction has fewer, and its blocks more room on
+// a CU.
+template <typename S>
+__host__ __device__ inline int ring_chunks(int64_t K) {
+    const int64_t mine = (K + S::KC * kWaves - 1) / (S::KC * kWaves);
+    return static_cast<int>(mine < S::RING ? mine : S::RING);
+}
+
 // 16-byte pieces of a segment XORed by this: a fragment read's 16 rows then touch
 // 16 different groups of four banks (segments are multiples of 256 bytes)
 __device__ __forceinline__ int seg_spread(int row) { return row & 15; }
@@ -60,7 +68,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_stream_kernel(MatmulArg
     // this wave's chunks: every kWaves-th
     const int chunks = (K + S::KC - 1) / S::KC;
     const int mine = (chunks - wave + kWaves - 1) / kWaves;
-    const uint32_t ring = lds_address(lds) + wave * (S::kChunk * S::RING);
+    const int rings = ring_chunks<S>(K);
+    const uint8_t* ring = lds + wave * (S::kChunk * rings);
+    const uint32_t ring_at = lds_address(ring);
 
     // a load covers kPerLoad rows: this lane's row in it, and its piece of the segment
     const int lrow = lane / S::kPieces, slot = lane % S::kPieces;
@@ -74,7 +84,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_stream_kernel(MatmulArg
     }
     auto request = [&](int c) __attribute__((always_inline)) {
         const int chunk = wave + c * kWaves;
-        const uint32_t to = ring + (c % S::RING) * S::kChunk;
+        const uint32_t to = ring_at + (c % S::RING) * S::kChunk;
         const int left = K - chunk * S::KC;
         const uint8_t* wc = w + static_cast<int64_t>(chunk) * S::kSeg;
         const uint8_t* xc = x + static_cast<int64_t>(chunk) * S::kSeg;
@@ -107,7 +117,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_stream_kernel(MatmulArg
         } else {
             wait_loads<0>();
         }
-        const uint8_t* p = lds + wave * (S::kChunk * S::RING) + (c % S::RING) * S::kChunk;
+        const uint8_t* p = ring + (c % S::RING) * S::kChunk;
 #pragma unroll
         for (int s = 0; s < S::KC / 32; ++s) {
             const bf16x8 fw = *reinterpret_cast<const bf16x8*>(
@@ -122,6 +132,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_stream_kernel(MatmulArg
 
     // waves' sums: [wave][row of x][n]
     __syncthreads();
+    static_assert(kWaves * 16 * kRowsN * 4 <= S::kChunk * kWaves, "sums fit the rings");
     float* part = reinterpret_cast<float*>(lds);
     *reinterpret_cast<f32x4*>(part + (wave * 16 + i16) * kRowsN + 4 * q) = acc[0] + acc[1];
     __syncthreads();
@@ -143,7 +154,7 @@ static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     const int64_t blocks = (a.P / S::MX + partial) * ((a.N + kRowsN - 1) / kRowsN);
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((matmul_stream_kernel<S, LINEAR>), dim3(static_cast<unsigned>(blocks)), dim3(64 * kWaves),
-                       S::kLds, stream, a);
+                       S::kChunk * ring_chunks<S>(a.K) * kWaves, stream, a);
     return hipGetLastError();
 }
 

@@ -87,25 +87,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_tile_kernel(MatmulArgs 
         next = next == RING - 1 ? 0 : next + 1;
     }
 
-    const int i16 = lane & 15, q = lane >> 4;
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-        if (!LINEAR && !a.accumulate && (S > 2 || a.out_fp32)) {
-            if (MODE == kDw && whole_lines(a, o.ldo))
-                store_rows<S / 2, true>(a, acc[i], o.out_row, o.ldo, o.col0, wm + 16 * i, o.rows, wn, o.cols, lane);
-            else
-                store_rows<S / 2, false>(a, acc[i], o.out_row, o.ldo, o.col0, wm + 16 * i, o.rows, wn, o.cols, lane);
-            continue;
-        }
-        const int row = wm + 16 * i + i16;
-#pragma unroll
-        for (int h = 0; h < S / 2; ++h) {
-            float v[8];
-            eight_columns(acc[i][2 * h], acc[i][2 * h + 1], v);
-            const int col = wn + 32 * h + eight_columns_at(q);
-            if (row < o.rows && col < o.cols) store8<LINEAR>(a, o.out_row + row, o.ldo, o.col0 + col, v);
-        }
-    }
+    store_all<MODE, LINEAR, S, S / 2>(a, acc, Place{o.out_row, o.ldo, o.col0, o.rows, wn, o.cols},
+                                      [&](int i) { return wm + 16 * i; }, lane);
 }
 
 template <int MODE, bool LINEAR, int T, int RING>
