@@ -347,7 +347,9 @@ enum moe_act {
 /*
  * Products grouped by expert. Rows offsets[e] .. offsets[e+1] - 1 of the row
  * matrices belong to group e (the `offsets` of moe_route; int32 [E+1] on the
- * device, ascending, within [0, P]); E in [1, MOE_MAX_EXPERTS]; E*N*K at most 2^39.
+ * device, ascending, within [0, P]); E in [1, MOE_MAX_EXPERTS]; E*N*K at most 2^39,
+ * E*P at most about 2^36 and E*P*max(N, K) at most about 2^46 (tiles are counted in
+ * 32 bits); more is MOE_ERR_INVALID_ARG.
  * A NULL `offsets` with E = 1 means one group of all P rows (a dense layer).
  *   moe_grouped_matmul:     y[s]  = x[s] W_e^T           x [P, K], w [E, N, K], y [P, N]
  *   moe_grouped_matmul_dx:  dx[s] = dy[s] W_e            dy [P, N], dx [P, K]
@@ -417,6 +419,9 @@ int moe_swiglu_backward(const uint16_t *dy, const uint16_t *z, int64_t rows, int
  *                      (then o is not read)
  * The gradient of residual is dy. An entry of perm or inv outside [0, T*top_k)
  * stands for a row of zeros (its d_gates is 0, and nothing of d_o is written for it).
+ * Any entries may repeat in moe_permute_rows and moe_combine; in moe_combine_backward
+ * a row of d_o that several entries name holds values of any of them, and one that
+ * none names is left as it was.
  */
 int moe_permute_rows(const uint16_t *x, const int32_t *perm, int64_t T, int32_t top_k,
                      int64_t d, uint16_t *xp, void *stream);

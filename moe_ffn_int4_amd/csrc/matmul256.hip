@@ -69,7 +69,7 @@ struct Group {
 constexpr int kTable = kMaxExperts * static_cast<int>(sizeof(Group));
 constexpr uint32_t kFewTiles = 32;
 
-// first of eighth x of n (the host refuses more than 2^26 tiles)
+// first of eighth x of n (the host refuses more than 2^30 tiles)
 __device__ __forceinline__ int eighth(uint32_t n, int x) { return static_cast<int>((n >> 3) * x + ((n & 7) * x >> 3)); }
 
 // tiles of BM rows, and whether a smaller one follows them
@@ -514,7 +514,7 @@ static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     // against 1554 us (forward 1301 against 1304).
     int64_t blocks = matmul256_blocks<MODE>(a);
     if ((MODE == kDw || a.E == 1) && blocks > 256) blocks = 256;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    if (blocks > kGridX) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((matmul256_kernel<MODE, LINEAR>), dim3(static_cast<unsigned>(blocks)),
                        dim3(64 * kWaves), kStages + kTable, stream, a);
     return hipGetLastError();

@@ -55,9 +55,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_stream_kernel(MatmulArg
     tiles.scan(a, lane);
     // blocks: the row tiles' 16-row strips of weights, tile after tile
     const int strips = static_cast<int>((a.N + kRowsN - 1) / kRowsN);
-    const int rt = blockIdx.x / strips;
+    const int block = static_cast<int>(block_index()), rt = block / strips;
     if (rt >= tiles.total) return;
-    const int n0 = (blockIdx.x - rt * strips) * kRowsN;
+    const int n0 = (block - rt * strips) * kRowsN;
     const MatTile t = tiles.find(rt, lane);
     const int nw = static_cast<int>(a.N - n0 < kRowsN ? a.N - n0 : kRowsN);
 
@@ -152,8 +152,7 @@ static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     if (ready != hipSuccess) return ready;
     const int64_t partial = a.E < a.P ? a.E : a.P;
     const int64_t blocks = (a.P / S::MX + partial) * ((a.N + kRowsN - 1) / kRowsN);
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((matmul_stream_kernel<S, LINEAR>), dim3(static_cast<unsigned>(blocks)), dim3(64 * kWaves),
+    hipLaunchKernelGGL((matmul_stream_kernel<S, LINEAR>), block_grid(blocks), dim3(64 * kWaves),
                        S::kChunk * ring_chunks<S>(a.K) * kWaves, stream, a);
     return hipGetLastError();
 }

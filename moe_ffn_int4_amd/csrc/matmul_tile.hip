@@ -99,7 +99,7 @@ static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
         hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (ready != hipSuccess) return ready;
     const int64_t blocks = matmul_blocks<MODE, T, T>(a);
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    if (blocks > 2 * kGridX) return hipErrorInvalidConfiguration;  // 256 threads each
     hipLaunchKernelGGL((matmul_tile_kernel<MODE, LINEAR, T, RING>), dim3(static_cast<unsigned>(blocks)),
                        dim3(64 * kWaves), kLds, stream, a);
     return hipGetLastError();

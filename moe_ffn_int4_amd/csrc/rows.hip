@@ -56,9 +56,9 @@ RowGrid row_grid(int64_t rows, int64_t pieces) {
 // this thread's row and piece; false past the end
 __device__ __forceinline__ bool row_piece(int64_t rows, int64_t pieces, int shift, unsigned chunks,
                                           int64_t& row, int64_t& piece) {
-    const unsigned b = blockIdx.x / chunks;
+    const unsigned block = block_index(), b = block / chunks;
     row = (static_cast<int64_t>(b) << (8 - shift)) + (threadIdx.x >> shift);
-    piece = (static_cast<int64_t>(blockIdx.x - b * chunks) << shift) + (threadIdx.x & ((1 << shift) - 1));
+    piece = (static_cast<int64_t>(block - b * chunks) << shift) + (threadIdx.x & ((1 << shift) - 1));
     return row < rows && piece < pieces;
 }
 static_assert(NT == 256, "row_piece: 2^8 threads");
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(NT) void swiglu_backward_kernel(const uint16_t* __r
 hipError_t launch_swiglu(const uint16_t* z, int64_t rows, int64_t h, uint16_t* y, hipStream_t stream) {
     const RowGrid g = row_grid(rows, h / 8);
     if (!g.ok) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(swiglu_kernel, dim3(g.blocks), dim3(NT), 0, stream, z, rows, h, g.shift, g.chunks, y);
+    hipLaunchKernelGGL(swiglu_kernel, block_grid(g.blocks), dim3(NT), 0, stream, z, rows, h, g.shift, g.chunks, y);
     return hipGetLastError();
 }
 
@@ -112,7 +112,7 @@ hipError_t launch_swiglu_backward(const uint16_t* dy, const uint16_t* z, int64_t
                                   uint16_t* dz, hipStream_t stream) {
     const RowGrid g = row_grid(rows, h / 8);
     if (!g.ok) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(swiglu_backward_kernel, dim3(g.blocks), dim3(NT), 0, stream, dy, z, rows, h, g.shift,
+    hipLaunchKernelGGL(swiglu_backward_kernel, block_grid(g.blocks), dim3(NT), 0, stream, dy, z, rows, h, g.shift,
                        g.chunks, dz);
     return hipGetLastError();
 }
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(NT) void combine_backward_kernel(const uint16_t* __
                                                               int top_k, int64_t d,
                                                               uint16_t* __restrict__ d_o,
                                                               float* __restrict__ d_gates) {
-    const int64_t pair = static_cast<int64_t>(blockIdx.x) * (NT / 64) + (threadIdx.x >> 6);
+    const int64_t pair = static_cast<int64_t>(block_index()) * (NT / 64) + (threadIdx.x >> 6);
     if (pair >= T * top_k) return;
     const int lane = threadIdx.x & 63;
     const int64_t t = pair / top_k;
@@ -327,7 +327,7 @@ hipError_t launch_permute_rows(const uint16_t* x, const int32_t* perm, int64_t T
                                uint16_t* xp, hipStream_t stream) {
     const RowGrid g = row_grid(T * top_k, d / 8);
     if (!g.ok) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(permute_rows_kernel, dim3(g.blocks), dim3(NT), 0, stream, x, perm, T, top_k, d, g.shift,
+    hipLaunchKernelGGL(permute_rows_kernel, block_grid(g.blocks), dim3(NT), 0, stream, x, perm, T, top_k, d, g.shift,
                        g.chunks, xp);
     return hipGetLastError();
 }
@@ -338,10 +338,10 @@ hipError_t launch_combine_rows(const void* o, bool o_fp32, const int32_t* inv, c
     const RowGrid g = row_grid(T, d / 8);
     if (!g.ok) return hipErrorInvalidConfiguration;
     if (o_fp32)
-        hipLaunchKernelGGL(combine_rows_kernel<float>, dim3(g.blocks), dim3(NT), 0, stream,
+        hipLaunchKernelGGL(combine_rows_kernel<float>, block_grid(g.blocks), dim3(NT), 0, stream,
                            static_cast<const float*>(o), inv, gates, residual, T, top_k, d, g.shift, g.chunks, y);
     else
-        hipLaunchKernelGGL(combine_rows_kernel<uint16_t>, dim3(g.blocks), dim3(NT), 0, stream,
+        hipLaunchKernelGGL(combine_rows_kernel<uint16_t>, block_grid(g.blocks), dim3(NT), 0, stream,
                            static_cast<const uint16_t*>(o), inv, gates, residual, T, top_k, d, g.shift, g.chunks, y);
     return hipGetLastError();
 }
@@ -350,8 +350,7 @@ hipError_t launch_combine_backward(const uint16_t* dy, const void* o, bool o_fp3
                                    const float* gates, int64_t T, int top_k, int64_t d, uint16_t* d_o,
                                    float* d_gates, hipStream_t stream) {
     const int64_t blocks = (T * top_k + NT / 64 - 1) / (NT / 64);
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    const dim3 grid(static_cast<unsigned>(blocks));
+    const dim3 grid = block_grid(blocks);
     if (o_fp32)
         hipLaunchKernelGGL(combine_backward_kernel<float>, grid, dim3(NT), 0, stream, dy,
                            static_cast<const float*>(o), inv, gates, T, top_k, d, d_o, d_gates);

@@ -54,6 +54,12 @@ int check_product(int64_t P, int64_t E, int64_t N, int64_t K, const int32_t* off
     CHECK(check_width(N, "N"));
     CHECK(check_width(K, "K"));
     if (E * N * K > (1LL << 39)) return fail(MOE_ERR_INVALID_ARG, "weights exceed 1 TiB");
+    // the kernels count tiles in 32 bits, also where offsets out of order make every
+    // group all P rows
+    const int64_t width = N > K ? N : K;
+    if (E * (P / 64 + 1) > (1LL << 30) || E * (P / 256 + 1) * (width / 256 + 1) > (1LL << 30))
+        return fail(MOE_ERR_INVALID_ARG, "P = %lld with E = %lld and %lld features: too many tiles", (long long)P,
+                    (long long)E, (long long)width);
     if (!offsets) {
         if (E != 1) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL with E = %lld", (long long)E);
         return MOE_OK;

@@ -37,6 +37,15 @@ hipError_t launch_matmul256(int mode, bool linear, const MatmulArgs& a, hipStrea
 hipError_t launch_matmul_stream(bool linear, const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_matmul(int mode, bool linear, const MatmulArgs& a, hipStream_t stream);
 
+// A launch has fewer than 2^32 threads along x: more blocks than kGridX stand in rows of
+// that many, the last of which may have blocks past the end.
+constexpr int64_t kGridX = 1 << 22;
+inline dim3 block_grid(int64_t blocks) {
+    if (blocks <= kGridX) return dim3(static_cast<unsigned>(blocks));
+    return dim3(static_cast<unsigned>(kGridX), static_cast<unsigned>((blocks + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ unsigned block_index() { return blockIdx.x + blockIdx.y * gridDim.x; }
+
 // two fp32 -> packed bf16 pair, round to nearest even, NaN kept
 __device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

@@ -1,0 +1,178 @@
+"""The training operators where calls can go wrong: sums into old values in every kernel, memory
+around the outputs, indices named twice, launches of more blocks than a grid row, streams."""
+import pytest
+import torch
+
+import moe_ffn_int4_amd as moe
+from train_util import DEV, HALF, U32, bf16, gen, offsets_of, product_bound, say, split_counts, within
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+OUT = [torch.bfloat16, torch.float32]
+
+# (P, E, N, K): tiles of 64, of 128 over four stages, of 128 over two, of 256
+KERNELS = [(90, 3, 136, 200), (700, 1, 1608, 1736), (700, 40, 392, 328), (2100, 2, 2904, 2904)]
+
+
+@pytest.mark.parametrize("out", OUT, ids=["bf16", "fp32"])
+@pytest.mark.parametrize("P,E,N,K", KERNELS)
+def test_dw_accumulates_in_every_kernel(P, E, N, K, out):
+    say(f"dw accumulate {P} {E} {N} {K} {out}")
+    g = gen(P + N)
+    counts = split_counts(P, E, 5)
+    off = offsets_of(counts)
+    dy, x = bf16(g, P, N).to(DEV), bf16(g, P, K).to(DEV)
+    dw = torch.randn(E, N, K, generator=g).to(out).to(DEV)
+    old = dw.double()
+    moe.grouped_matmul_dw(dy, x, off.to(DEV), out=dw, accumulate=True)
+    for e in range(E):
+        s = slice(int(off[e]), int(off[e + 1]))
+        a, b = dy[s].double().t(), x[s].double()
+        ref, size = a @ b + old[e], a.abs() @ b.abs() + old[e].abs()
+        within(dw[e], ref, product_bound(ref, size, counts[e] + 1, out), f"dw[{e}]")
+
+
+@pytest.mark.parametrize("out", OUT, ids=["bf16", "fp32"])
+@pytest.mark.parametrize("P,E,N,K", [(3, 1, 264, 136), (16, 8, 264, 136), (60, 20, 72, 136)] + KERNELS)
+def test_memory_around_the_outputs_is_left(P, E, N, K, out):
+    """Outputs that stand inside a larger buffer, 16-byte aligned only: what is around them stays."""
+    say(f"around {P} {E} {N} {K} {out}")
+    g = gen(P + K)
+    off = offsets_of(split_counts(P, E, 6)).to(DEV)
+    x, w, dy = bf16(g, P, K).to(DEV), bf16(g, E, N, K, scale=0.1).to(DEV), bf16(g, P, N).to(DEV)
+    r, b = bf16(g, P, N).to(DEV), torch.randn(N, generator=g).to(DEV)
+    pad = 4104  # values: a multiple of 8, of no larger power of two
+
+    def inside(shape, dtype):
+        n = 1
+        for v in shape:
+            n *= v
+        buf = torch.full((n + 2 * pad,), 7.0, dtype=dtype, device=DEV)
+        return buf, buf[pad:pad + n].view(shape)
+
+    z = inside((P, N), BF)
+    for what, shape, call in [
+            ("y", (P, N), lambda o: moe.grouped_matmul(x, w, off, out=o)),
+            ("dx", (P, K), lambda o: moe.grouped_matmul_dx(dy, w, off, out=o)),
+            ("dw", (E, N, K), lambda o: moe.grouped_matmul_dw(dy, x, off, out=o)),
+            ("linear", (P, N), lambda o: moe.linear(x, w[0], b, "silu", r, z[1], out=o)),
+            ("linear plain", (P, N), lambda o: moe.linear(x, w[0], out=o))]:
+        buf, view = inside(shape, out)
+        apart = torch.empty(shape, dtype=out, device=DEV)
+        call(view)
+        assert bool((buf[:pad] == 7).all()) and bool((buf[-pad:] == 7).all()), what
+        call(apart)
+        assert torch.equal(apart, view), what
+    assert bool((z[0][:pad] == 7).all()) and bool((z[0][-pad:] == 7).all())
+
+
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("T,N,K", [(500, 1608, 520), (3000, 2104, 200)])
+def test_linear_into_its_residual_in_large_tiles(T, N, K, act):
+    g = gen(T)
+    x, w, r = bf16(g, T, K).to(DEV), bf16(g, N, K, scale=0.1).to(DEV), bf16(g, T, N).to(DEV)
+    b = torch.randn(N, generator=g).to(DEV)
+    apart = moe.linear(x, w, b, act, r)
+    assert torch.equal(moe.linear(x, w, b, act, r, out=r), apart)
+
+
+@pytest.mark.parametrize("T,k,d", [(9, 5, 72), (40, 7, 264), (130, 6, 1032)])
+def test_combine_of_any_number_of_rows(T, k, d):
+    g = gen(T)
+    inv = torch.randperm(T * k, generator=g).to(torch.int32).view(T, k)
+    o, gates = bf16(g, T * k, d), torch.randn(T, k, generator=g)
+    terms = o.double()[inv.long()] * gates.double().unsqueeze(2)
+    ref, err = terms.sum(1), (k + 1) * U32 * terms.abs().sum(1)
+    within(moe.combine(o.to(DEV), inv.to(DEV), gates.to(DEV)), ref, err + HALF[BF] * (ref.abs() + err), "y")
+
+
+def test_indices_named_twice():
+    """permute_rows and combine read a row as often as it is named; combine_backward writes
+    values of one of the pairs that name a row."""
+    T, k, d = 50, 4, 136
+    g = gen(8)
+    x, dy = bf16(g, T, d), bf16(g, T, d)
+    perm = torch.randint(0, T * k, (T * k,), generator=g).to(torch.int32)
+    assert torch.equal(moe.permute_rows(x.to(DEV), perm.to(DEV), k).cpu(), x[perm.long() // k])
+    inv = torch.randint(0, 20, (T, k), generator=g).to(torch.int32)
+    o, gates = bf16(g, T * k, d), torch.rand(T, k, generator=g)
+    terms = o.double()[inv.long()] * gates.double().unsqueeze(2)
+    ref, err = terms.sum(1), (k + 1) * U32 * terms.abs().sum(1)
+    within(moe.combine(o.to(DEV), inv.to(DEV), gates.to(DEV)), ref, err + HALF[BF] * (ref.abs() + err), "y")
+    d_o = torch.full((T * k, d), 7.0, dtype=BF, device=DEV)
+    _, dg = moe.combine_backward(dy.to(DEV), o.to(DEV), inv.to(DEV), gates.to(DEV), out=d_o)
+    prod = dy.double().unsqueeze(1) * o.double()[inv.long()]
+    within(dg, prod.sum(2), (d + 1) * U32 * prod.abs().sum(2), "d_gates")
+    d_o = d_o.cpu()
+    each = (gates.unsqueeze(2) * dy.float().unsqueeze(1)).to(BF)
+    for slot in range(20):
+        named = each[inv == slot]
+        assert bool((named == d_o[slot]).any(0).all()), slot
+    assert bool((d_o[20:] == 7).all())
+
+
+def test_more_pairs_than_threads_of_a_grid_row():
+    """A wave for each of more than 2^26 pairs."""
+    T, k, d = (1 << 22) + 5, 16, 8
+    say(f"combine_backward of {T * k} pairs")
+    dy = torch.randn(T, d, device=DEV).to(BF)
+    gates = torch.rand(T, k, device=DEV)
+    inv = torch.arange(T * k, dtype=torch.int32, device=DEV).view(T, k)
+    o = torch.randn(T * k, d, device=DEV, dtype=BF)
+    d_o, dg = moe.combine_backward(dy, o, inv, gates)
+    # one product in fp32 and one rounding: the same bits
+    assert torch.equal(d_o.view(T, k, d), (gates.unsqueeze(2) * dy.float().unsqueeze(1)).to(BF))
+    for s in (slice(0, 1000), slice(T - 1000, T)):
+        prod = dy[s].double().unsqueeze(1) * o.view(T, k, d)[s].double()
+        within(dg[s], prod.sum(2), (d + 1) * U32 * prod.abs().sum(2), "d_gates")
+
+
+def test_more_blocks_than_a_grid_row():
+    # the streaming product: 512 row tiles of 8193 strips
+    E, P, N, K = 256, 1024, (1 << 17) + 8, 8
+    say(f"grouped_matmul {P} {E} {N} {K}")
+    x, w = torch.randn(P, K, device=DEV).to(BF), torch.randn(E, N, K, device=DEV).to(BF)
+    off = torch.arange(0, P + 1, 4, dtype=torch.int32, device=DEV)
+    y = moe.grouped_matmul(x, w, off)
+    for c in (slice(0, 64), slice(N - 200, N)):
+        wide = w[:, c].double().transpose(1, 2).contiguous()
+        rows = x.double().view(E, 4, K)
+        ref, size = torch.bmm(rows, wide).view(P, -1), torch.bmm(rows.abs(), wide.abs()).view(P, -1)
+        within(y[:, c], ref, product_bound(ref, size, K, BF), "y")
+    del x, w, y
+    # rows of five pieces of 256 threads
+    rows, h = 1 << 20, 8200
+    say(f"swiglu {rows} {h}")
+    z = torch.empty(rows, 2 * h, dtype=BF, device=DEV).normal_()
+    y = torch.full((rows, h), 7.0, dtype=BF, device=DEV)
+    moe.swiglu(z, out=y)
+    for s in (slice(0, 300), slice(rows // 2, rows // 2 + 300), slice(rows - 300, rows)):
+        assert torch.equal(y[s], moe.swiglu(z[s])), s
+
+
+def test_row_operators_on_two_streams():
+    T, k, d = 300, 4, 520
+    g = gen(2)
+    inv = torch.randperm(T * k, generator=g).to(torch.int32).to(DEV)
+    perm = torch.argsort(inv).to(torch.int32)
+    inv = inv.view(T, k)
+    x, z, gates = bf16(g, T, d).to(DEV), bf16(g, T, 2 * d).to(DEV), torch.rand(T, k, generator=g).to(DEV)
+
+    def run():
+        xp = moe.permute_rows(x, perm, k)
+        y = moe.combine(xp, inv, gates, x)
+        return [xp, y, *moe.combine_backward(y, xp, inv, gates), moe.swiglu(z), moe.swiglu_backward(y, z),
+                *moe.linear_dz(y, x, "silu")]
+
+    first = run()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(run())
+    torch.cuda.synchronize()
+    for outs in got:
+        for a, e in zip(outs, first):
+            assert torch.equal(a, e)

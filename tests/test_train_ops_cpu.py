@@ -148,3 +148,13 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         moe.combine(x.half(), off)
     with pytest.raises(ValueError, match="act"):
         moe._act("tanh")
+
+
+@pytest.mark.parametrize("which", ["fwd", "dx", "dw"])
+@pytest.mark.parametrize("kw", [dict(E=256, P=1 << 30, N=8, K=8), dict(E=256, P=1 << 26, N=1 << 20, K=8),
+                                dict(E=256, P=1 << 26, N=8, K=1 << 20)])
+def test_more_tiles_than_the_kernels_count(L, which, kw):
+    """Offsets out of order may make every group all P rows: their tiles have to be countable."""
+    spread = {n: F + i * (1 << 52) for i, n in enumerate(("a", "b", "off", "out"))}
+    assert _grouped(L, which, **spread, **kw) == INVALID
+    assert "too many tiles" in _said(L), _said(L)
