@@ -5,6 +5,11 @@
 // in 64-deep steps through a ring of LDS stages: step k + RING - 1 is requested, straight
 // to LDS, while step k is multiplied, one barrier a step. With 64 KB of LDS two blocks
 // share a CU, and one block's loads and barriers overlap the other's products.
+//
+// KS parts of the reduction: a block of KS x 4 waves takes every KS-th step in each part,
+// with a ring of its own, and adds the parts' sums in order. Few tiles leave a CU one
+// block, whose steps then wait for HBM: 17 x 64 x 5120, a single tile, takes 350 ns a
+// step with three requested ahead, and 20 us instead of 28 with three parts.
 #include "matmul.h"
 
 namespace moe {
@@ -25,14 +30,15 @@ __device__ __forceinline__ void wait_steps(int steps) {
 }
 }  // namespace
 
-template <int MODE, bool LINEAR, int T, int RING>
-__global__ __launch_bounds__(64 * kWaves, 2) void matmul_tile_kernel(MatmulArgs a) {
+template <int MODE, bool LINEAR, int T, int RING, int KS>
+__global__ __launch_bounds__(64 * kWaves * KS, KS == 1 ? 2 : KS) void matmul_tile_kernel(MatmulArgs a) {
     constexpr int kTile = T * kStepR * 2;  // one operand of one step
     constexpr int kStage = 2 * kTile;
     constexpr int S = T / 32;              // 16-wide sub-tiles of a wave, each way
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & (kWaves - 1);
+    const int part = __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * kWaves));
     MatTile t;
     int rt, ct;
     if (!find_tile<MODE, T, T, kBand>(a, lane, t, rt, ct)) return;
@@ -55,22 +61,30 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_tile_kernel(MatmulArgs 
 #pragma unroll
         for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int steps = static_cast<int>((o.red + kStepR - 1) / kStepR);
-    const uint32_t at = lds_address(lds);
+    const int all = static_cast<int>((o.red + kStepR - 1) / kStepR);
+    const int steps = (all - part + KS - 1) / KS, most = (all + KS - 1) / KS;  // this part's, and any's
+    const uint8_t* ring = lds + part * (RING * kStage);
+    const uint32_t at = lds_address(ring);
     constexpr int kLoads = 2 * T / 8 / kWaves;  // a wave's, a step
+    // A's first 32 rows alone where the tile has no more (a wave's first load of two; what LDS
+    // holds of the others goes into rows that are not stored): 17 x 16384 x 5120 dx 53.7 -> 51.4 us
+    const bool half = MODE != kDw && T == 64 && o.rows <= 32;
     auto request = [&](int stage, int k) __attribute__((always_inline)) {
-        sa.load(at + stage * kStage, k, o.red);
-        sb.load(at + stage * kStage + kTile, k, o.red);
+        if (half) sa.template load<0, T / 64>(at + stage * kStage, part + k * KS, o.red);
+        else sa.load(at + stage * kStage, part + k * KS, o.red);
+        sb.load(at + stage * kStage + kTile, part + k * KS, o.red);
     };
     for (int k = 0; k < RING - 1 && k < steps; ++k) request(k, k);
     int cur = 0, next = RING - 1;  // stages of step k and of step k + RING - 1
-    for (int k = 0; k < steps; ++k) {
+    for (int k = 0; k < most; ++k) {
         // step k has landed (steps k + 1 .. k + RING - 2 may be under way), and every
         // wave has read step k - 1, whose stage is the next to be written
-        wait_steps<kLoads, RING - 2>(steps - 1 - k);
+        if (half) wait_steps<kLoads - T / 64, RING - 2>(steps - 1 - k);
+        else wait_steps<kLoads, RING - 2>(steps - 1 - k);
         __syncthreads();
+        if (KS > 1 && k >= steps) break;  // the last round, of fewer parts
         if (k + RING - 1 < steps) request(next, k + RING - 1);
-        const uint8_t* p = lds + cur * kStage;
+        const uint8_t* p = ring + cur * kStage;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             bf16x8 fa[S], fb[S];
@@ -87,29 +101,49 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_tile_kernel(MatmulArgs 
         next = next == RING - 1 ? 0 : next + 1;
     }
 
+    if (KS > 1) {
+        // the other parts' sums, in order, through LDS
+        __syncthreads();
+        f32x4* sums = reinterpret_cast<f32x4*>(lds) + threadIdx.x % (64 * kWaves);
+#pragma unroll
+        for (int p = 1; p < KS; ++p) {
+            f32x4* mine = sums + (p - 1) * (S * S * 64 * kWaves);
+            if (part == p) {
+#pragma unroll
+                for (int i = 0; i < S * S; ++i) mine[i * 64 * kWaves] = acc[i / S][i % S];
+            }
+        }
+        __syncthreads();
+        if (part > 0) return;
+#pragma unroll
+        for (int p = 1; p < KS; ++p)
+#pragma unroll
+            for (int i = 0; i < S * S; ++i) acc[i / S][i % S] += sums[((p - 1) * S * S + i) * 64 * kWaves];
+    }
+
     store_all<MODE, LINEAR, S, S / 2>(a, acc, Place{o.out_row, o.ldo, o.col0, o.rows, wn, o.cols},
                                       [&](int i) { return wm + 16 * i; }, lane);
 }
 
-template <int MODE, bool LINEAR, int T, int RING>
+template <int MODE, bool LINEAR, int T, int RING, int KS>
 static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
-    constexpr int kLds = RING * 2 * T * kStepR * 2;
+    constexpr int kLds = KS * RING * 2 * T * kStepR * 2;
     static const hipError_t ready = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(&matmul_tile_kernel<MODE, LINEAR, T, RING>),
+        reinterpret_cast<const void*>(&matmul_tile_kernel<MODE, LINEAR, T, RING, KS>),
         hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (ready != hipSuccess) return ready;
     const int64_t blocks = matmul_blocks<MODE, T, T>(a);
     if (blocks > 2 * kGridX) return hipErrorInvalidConfiguration;  // 256 threads each
-    hipLaunchKernelGGL((matmul_tile_kernel<MODE, LINEAR, T, RING>), dim3(static_cast<unsigned>(blocks)),
-                       dim3(64 * kWaves), kLds, stream, a);
+    hipLaunchKernelGGL((matmul_tile_kernel<MODE, LINEAR, T, RING, KS>), dim3(static_cast<unsigned>(blocks)),
+                       dim3(64 * kWaves * KS), kLds, stream, a);
     return hipGetLastError();
 }
 
 template <int T, int RING>
 static hipError_t launch_tile(int mode, bool linear, const MatmulArgs& a, hipStream_t stream) {
-    if (mode == kDx) return launch<kDx, false, T, RING>(a, stream);
-    if (mode == kDw) return launch<kDw, false, T, RING>(a, stream);
-    return linear ? launch<kFwd, true, T, RING>(a, stream) : launch<kFwd, false, T, RING>(a, stream);
+    if (mode == kDx) return launch<kDx, false, T, RING, 1>(a, stream);
+    if (mode == kDw) return launch<kDw, false, T, RING, 1>(a, stream);
+    return linear ? launch<kFwd, true, T, RING, 1>(a, stream) : launch<kFwd, false, T, RING, 1>(a, stream);
 }
 
 // Tiles of T x T, an estimate where the host does not know the group sizes: each
@@ -127,7 +161,12 @@ static int64_t tiles(int mode, const MatmulArgs& a, int64_t T) {
 //   * few rows, y = x W^T: the streaming kernel. 1 x 8192 x 5120: 17 against 29 in tiles
 //     of 64; 16 rows: 19 against 29; 32 rows: 29 against 30. 16 rows over E = 16 of
 //     16384 x 5120: 424 against 434 in tiles of 256; 64 rows: 461 against 434.
-//   * up to 512 tiles of 64: those. 64 x 8192 x 5120: 32 (128: 58, 256: 85); 256 x 8192 x
+//   * up to 256 tiles of 64 and a reduction of 1024 or more, not weight gradients: those,
+//     in three parts. 100 x 4096 x 4096 (128 tiles): 16.1 against 23.5 in one part, in two
+//     18.4; 256 x 4096 x 4096 (256): 21.6 (24.5); 17 x 8192 x 5120 (128): 24.3 (30.0);
+//     256 x 8192 x 5120 (512): 54.1 (51.6); 300 rows over E = 16, 512 x 1024, dx, of
+//     length 512: 7.6 (6.7).
+//   * up to 512 tiles of 64: those, in one part. 64 x 8192 x 5120: 32 (128: 58, 256: 85); 256 x 8192 x
 //     5120 (512 tiles): 53 (63, 89); 512 x 8192 x 5120 (1024): 92 (66, 86); 2048 x 1024 x
 //     1024 (512): 14 (21, 25).
 //   * up to 256 tiles of 128: those, one block a CU, over four stages (three steps
@@ -141,9 +180,13 @@ static int64_t tiles(int mode, const MatmulArgs& a, int64_t T) {
 //     115 (132).
 hipError_t launch_matmul(int mode, bool linear, const MatmulArgs& a, hipStream_t stream) {
     if (mode == kFwd && (a.P <= 16 || a.P <= 4 * a.E)) return launch_matmul_stream(linear, a, stream);
+    if (mode != kDw && (mode == kFwd ? a.K : a.N) >= 1024 && tiles(mode, a, 64) <= 256) {
+        if (mode == kDx) return launch<kDx, false, 64, 3, 3>(a, stream);
+        return linear ? launch<kFwd, true, 64, 3, 3>(a, stream) : launch<kFwd, false, 64, 3, 3>(a, stream);
+    }
     if (tiles(mode, a, 64) <= 512) return launch_tile<64, 4>(mode, linear, a, stream);
     if (tiles(mode, a, 128) <= 256) return launch_tile<128, 4>(mode, linear, a, stream);
-    if (mode == kDw && a.P < 384 * a.E) return launch<kDw, false, 128, 2>(a, stream);
+    if (mode == kDw && a.P < 384 * a.E) return launch<kDw, false, 128, 2, 1>(a, stream);
     return launch_matmul256(mode, linear, a, stream);
 }
 

@@ -176,3 +176,31 @@ def test_row_operators_on_two_streams():
     for outs in got:
         for a, e in zip(outs, first):
             assert torch.equal(a, e)
+
+
+@pytest.mark.parametrize("R", [1024, 1032, 1096, 1160, 2040])
+@pytest.mark.parametrize("counts", [(17,), (32,), (33,), (20, 0, 64, 65, 1, 31), (150, 3)])
+def test_few_tiles_of_long_reductions(counts, R):
+    """The reduction in three parts of a block: steps that divide by three and that do not, row
+    tiles of at most 32 rows and of more, a last step that is not whole."""
+    P, E, N = sum(counts), len(counts), 136
+    g = gen(R + P)
+    off = offsets_of(counts)
+    x, w = bf16(g, P, R), bf16(g, E, N, R, scale=0.1)
+    v = bf16(g, E, R, N, scale=0.1)
+    y = moe.grouped_matmul(x.to(DEV), w.to(DEV), off.to(DEV), out_dtype=torch.float32)
+    dx = moe.grouped_matmul_dx(x.to(DEV), v.to(DEV), off.to(DEV), out_dtype=torch.float32)
+    for e in range(E):
+        s = slice(int(off[e]), int(off[e + 1]))
+        a = x[s].double()
+        for got, b in ((y[s], w[e].double().t()), (dx[s], v[e].double())):
+            ref, size = a @ b, a.abs() @ b.abs()
+            within(got, ref, product_bound(ref, size, R, torch.float32), f"group {e}")
+    if E > 1:
+        return
+    b, r = torch.randn(N, generator=g), bf16(g, P, N)
+    y = moe.linear(x.to(DEV), w[0].to(DEV), b.to(DEV), "relu", r.to(DEV))
+    pre = x.double() @ w[0].double().t() + b.double()
+    err = (R + 3) * U32 * (x.double().abs() @ w[0].double().abs().t() + b.double().abs() + r.double().abs())
+    ref = pre.clamp(min=0) + r.double()
+    within(y, ref, err + HALF[BF] * (ref.abs() + err), "linear")
