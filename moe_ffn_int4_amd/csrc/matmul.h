@@ -62,6 +62,13 @@ __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// A value that is the same in all lanes, for a scalar register.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+    return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 // ---------------------------------------------------------------- tile lookup
 
 struct MatTile {
@@ -246,7 +253,7 @@ struct Stager {
     __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int valid, int wave_, int lane_) {
         wave = wave_;
         lane = lane_;
-        base = reinterpret_cast<const uint8_t*>(p);
+        base = reinterpret_cast<const uint8_t*>(uniform(reinterpret_cast<uint64_t>(p)));
         step = TR ? kStepR * ld * 2 : kStepR * 2;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {

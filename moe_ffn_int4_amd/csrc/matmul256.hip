@@ -211,13 +211,6 @@ __device__ __forceinline__ bool find(const MatmulArgs& a, const Group* table, in
     return true;
 }
 
-// A value that is the same in all lanes, for a scalar register.
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
-    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
-    return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
-}
-
 // Half `h` of an operand: index i (0..127) in the half -> index in the tile. Of A the
 // first 64 are the rows of waves 0..3 and the last those of waves 4..7, `each` rows
 // apart (64, or fewer in the last half of a tile's rows).

@@ -1,5 +1,5 @@
-// matmul_stream.hip -- y[s] = x[s] W_e^T for groups of a few rows: the weights of every
-// group with rows are read once, and reading them is all that costs.
+// matmul_stream.hip -- y[s] = x[s] W_e^T for groups of a few rows, where reading the
+// weights once is all that costs, and for small outputs, whose few blocks wait least here.
 //
 // A block takes 16 weight rows (outputs n) and up to MX rows of x; its four waves
 // split the reduction, each streaming its quarter through a ring of its own in LDS (no

@@ -139,54 +139,64 @@ static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int T, int RING>
+template <int T, int RING, int KS>
 static hipError_t launch_tile(int mode, bool linear, const MatmulArgs& a, hipStream_t stream) {
-    if (mode == kDx) return launch<kDx, false, T, RING, 1>(a, stream);
-    if (mode == kDw) return launch<kDw, false, T, RING, 1>(a, stream);
-    return linear ? launch<kFwd, true, T, RING, 1>(a, stream) : launch<kFwd, false, T, RING, 1>(a, stream);
+    if (mode == kDx) return launch<kDx, false, T, RING, KS>(a, stream);
+    if (mode == kDw) return launch<kDw, false, T, RING, KS>(a, stream);
+    return linear ? launch<kFwd, true, T, RING, KS>(a, stream) : launch<kFwd, false, T, RING, KS>(a, stream);
 }
 
-// Tiles of T x T, an estimate where the host does not know the group sizes: each
-// group's last row tile is half empty.
+// Row tiles of T, an estimate where the host does not know the group sizes: each group's
+// last one is half empty.
+static int64_t row_tiles(const MatmulArgs& a, int64_t T) {
+    const int64_t groups = a.E < a.P ? a.E : a.P;
+    return groups == 1 ? (a.P + T - 1) / T : a.P / T + (groups + 1) / 2;
+}
+
 static int64_t tiles(int mode, const MatmulArgs& a, int64_t T) {
     auto up = [T](int64_t v) { return (v + T - 1) / T; };
     if (mode == kDw) return a.E * up(a.N) * up(a.K);
-    const int64_t groups = a.E < a.P ? a.E : a.P;
-    const int64_t rows = groups == 1 ? up(a.P) : a.P / T + (groups + 1) / 2;
-    return rows * up(mode == kFwd ? a.N : a.K);
+    return row_tiles(a, T) * up(mode == kFwd ? a.N : a.K);
 }
 
 // The kernel for a product. What decides is how many tiles there are for the chip's
-// 256 CUs, and (us, measured at rows x N x K, dense unless E experts are named):
-//   * few rows, y = x W^T: the streaming kernel. 1 x 8192 x 5120: 17 against 29 in tiles
-//     of 64; 16 rows: 19 against 29; 32 rows: 29 against 30. 16 rows over E = 16 of
-//     16384 x 5120: 424 against 434 in tiles of 256; 64 rows: 461 against 434.
-//   * up to 256 tiles of 64 and a reduction of 1024 or more, not weight gradients: those,
-//     in three parts. 100 x 4096 x 4096 (128 tiles): 16.1 against 23.5 in one part, in two
-//     18.4; 256 x 4096 x 4096 (256): 21.6 (24.5); 17 x 8192 x 5120 (128): 24.3 (30.0);
-//     256 x 8192 x 5120 (512): 54.1 (51.6); 300 rows over E = 16, 512 x 1024, dx, of
-//     length 512: 7.6 (6.7).
-//   * up to 512 tiles of 64: those, in one part. 64 x 8192 x 5120: 32 (128: 58, 256: 85); 256 x 8192 x
-//     5120 (512 tiles): 53 (63, 89); 512 x 8192 x 5120 (1024): 92 (66, 86); 2048 x 1024 x
-//     1024 (512): 14 (21, 25).
-//   * up to 256 tiles of 128: those, one block a CU, over four stages (three steps
-//     ahead; two stages and two blocks: 81). 512 x 8192 x 5120 (256): 66; 1024 x 8192 x
-//     5120 (512): 124 against 92 in tiles of 256.
-//   * weight gradients of short reductions, whose time is the stores: tiles of 128,
-//     two blocks a CU. 20 rows in each of E = 128, 1000 x 712: 44 (256: 49); 64 rows in
-//     each of E = 8, 2048 x 1024: 10 (14); 512 rows in each of E = 16, 5120 x 8192: 834
-//     against 770 in tiles of 256.
-//   * else tiles of 256. 4096 x 2048 x 1024 (128): 29 (128: 30); 1024 x 5120 x 8192 (80):
-//     115 (132).
+// 256 CUs and how long the reduction is (of weight gradients: a group's mean). In us,
+// rows x N x K, dense unless E experts are named:
+//   * y = x W^T of up to 768 blocks of the streaming kernel: that. 58 x 472 x 4592 (120):
+//     8.2 against 19.6 in tiles of 64, split; 496 x 120 x 5328 (248): 10.0 (21.7).
+//     Also of a few rows, at least 2048 long, whatever the blocks: 16 rows over E = 16,
+//     16384 x 5120: 306 against 424 in tiles of 64; but 64 over E = 16, 4880 x 1704: 70
+//     (46), and 72 over E = 128, 9408 x 104: 112, in tiles of 128 over two stages 42.
+//   * up to 256 tiles of 64 and a reduction of 768 or more: those, split in three. 100 x
+//     4096 x 4096 (128 tiles): 16.1 against 23.5 not split, 18.4 split in two; 256 x 4096 x
+//     4096 (256): 21.6 (24.5); 17 x 8192 x 5120 (128): 24.3 (30.0; streaming, 1024 blocks: 29);
+//     256 x 8192 x 5120 (512): 54.1 (51.6); 8753 x 320 x 136, dW: 34 (46); 300 rows over E = 16,
+//     512 x 1024, dx, 512 long: 7.6 (6.7).
+//   * up to 512 tiles of 64: those. 256 x 8192 x 5120 (512 tiles): 52 (tiles of 128: 63, of
+//     256: 89); 512 x 8192 x 5120 (1024): 92 (66, 86).
+//   * up to 256 tiles of 128 and a reduction of 512 or more: those, one block a CU, over four
+//     stages (three steps ahead). 512 x 8192 x 5120 (256): 66, with two stages and two
+//     blocks a CU 81; 1024 x 8192 x 5120 (512): 124 against 92 in tiles of 256; 161 rows over E =
+//     8, 240 x 6208, dx: 13.6, with two stages 9.3.
+//   * reductions below 512 or groups of fewer than 128 rows, whose time is the start and
+//     the stores: tiles of 128 over two stages, two blocks a CU. 885 x 8248 x 504: 17
+//     (tiles of 256: 24); 2312 rows over E = 128, 1192 x 1008, dx: 59 (83); dW of 20 rows in
+//     each of E = 128, 1000 x 712: 44 (49); 8946 rows over E = 2, 11000 x 728: 205 (177);
+//     dW of 512 rows in each of E = 16, 5120 x 8192: 834 (770).
+//   * else tiles of 256. 1024 x 5120 x 8192 (80): 115 (128: 132).
+// Over 1300 products of random sizes this takes 2 % longer than the best kernel for each.
 hipError_t launch_matmul(int mode, bool linear, const MatmulArgs& a, hipStream_t stream) {
-    if (mode == kFwd && (a.P <= 16 || a.P <= 4 * a.E)) return launch_matmul_stream(linear, a, stream);
-    if (mode != kDw && (mode == kFwd ? a.K : a.N) >= 1024 && tiles(mode, a, 64) <= 256) {
-        if (mode == kDx) return launch<kDx, false, 64, 3, 3>(a, stream);
-        return linear ? launch<kFwd, true, 64, 3, 3>(a, stream) : launch<kFwd, false, 64, 3, 3>(a, stream);
+    const int64_t red = mode == kFwd ? a.K : mode == kDx ? a.N : a.P / a.E;
+    if (mode == kFwd) {
+        const bool few = a.P <= 16 || a.P <= 4 * a.E;
+        const int64_t blocks = row_tiles(a, a.P <= 4 * a.E ? 4 : 16) * ((a.N + 15) / 16);
+        if (blocks <= 768 || (few && red >= 2048)) return launch_matmul_stream(linear, a, stream);
     }
-    if (tiles(mode, a, 64) <= 512) return launch_tile<64, 4>(mode, linear, a, stream);
-    if (tiles(mode, a, 128) <= 256) return launch_tile<128, 4>(mode, linear, a, stream);
-    if (mode == kDw && a.P < 384 * a.E) return launch<kDw, false, 128, 2, 1>(a, stream);
+    const int64_t tiles64 = tiles(mode, a, 64);
+    if (red >= 768 && tiles64 <= 256) return launch_tile<64, 3, 3>(mode, linear, a, stream);
+    if (tiles64 <= 512) return launch_tile<64, 4, 1>(mode, linear, a, stream);
+    if (red >= 512 && tiles(mode, a, 128) <= 256) return launch_tile<128, 4, 1>(mode, linear, a, stream);
+    if (red < 512 || a.P < 128 * a.E) return launch_tile<128, 2, 1>(mode, linear, a, stream);
     return launch_matmul256(mode, linear, a, stream);
 }
 

@@ -204,3 +204,30 @@ def test_few_tiles_of_long_reductions(counts, R):
     err = (R + 3) * U32 * (x.double().abs() @ w[0].double().abs().t() + b.double().abs() + r.double().abs())
     ref = pre.clamp(min=0) + r.double()
     within(y, ref, err + HALF[BF] * (ref.abs() + err), "linear")
+
+
+@pytest.mark.parametrize("counts,N,R", [((30,), 6152, 1032), ((300,), 1096, 1000), ((33, 0, 90, 140), 1096, 776),
+                                        ((2000,), 264, 8)])
+def test_forward_of_long_reductions_and_many_columns(counts, N, R):
+    """As above, for outputs too wide for the streaming product; and weight gradients of so many rows."""
+    P, E = sum(counts), len(counts)
+    g = gen(R + P)
+    off = offsets_of(counts)
+    x, w, dy = bf16(g, P, R), bf16(g, E, N, R, scale=0.1), bf16(g, P, N)
+    y = moe.grouped_matmul(x.to(DEV), w.to(DEV), off.to(DEV))
+    dw = moe.grouped_matmul_dw(dy.to(DEV), x.to(DEV), off.to(DEV), out_dtype=torch.float32)
+    for e in range(E):
+        s = slice(int(off[e]), int(off[e + 1]))
+        for got, a, b, red, out in ((y[s], x[s].double(), w[e].double().t(), R, BF),
+                                    (dw[e], dy[s].double().t(), x[s].double(), counts[e], torch.float32)):
+            ref, size = a @ b, a.abs() @ b.abs()
+            within(got, ref, product_bound(ref, size, red, out), f"group {e}")
+    if E > 1:
+        return
+    b, r, z = torch.randn(N, generator=g), bf16(g, P, N), torch.empty(P, N, dtype=BF, device=DEV)
+    y = moe.linear(x.to(DEV), w[0].to(DEV), b.to(DEV), "relu", r.to(DEV), z, out_dtype=torch.float32)
+    pre = x.double() @ w[0].double().t() + b.double()
+    err = (R + 3) * U32 * (x.double().abs() @ w[0].double().abs().t() + b.double().abs() + r.double().abs())
+    ref = pre.clamp(min=0) + r.double()
+    within(y, ref, err + HALF[torch.float32] * (ref.abs() + err), "linear")
+    within(z, pre, err + HALF[BF] * (pre.abs() + err), "z")
