@@ -149,6 +149,14 @@ struct RowTiles {
     }
 };
 
+// Row tile rt of one group of all rows: nothing to read before the first request (a dense
+// 1 x 8192 x 5120: 14.4 against 14.9 us).
+template <int BM>
+__device__ __forceinline__ MatTile dense_tile(const MatmulArgs& a, int rt) {
+    const int64_t row0 = static_cast<int64_t>(rt) * BM, left = a.P - row0;
+    return MatTile{0, row0, static_cast<int>(left < BM ? left : BM)};
+}
+
 // Block -> tile. Blocks are dealt to the 8 XCDs round robin, and each XCD takes
 // a contiguous range of the tiles, so that the tiles it runs at once share operand
 // panels in its L2. Inside a range the walk takes BAND row tiles down each column
@@ -190,12 +198,13 @@ __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int lane, MatTile
         return !(a.accumulate && t.nrows == 0);
     }
     RowTiles<BM> tiles;
-    tiles.scan(a, lane);
+    if (a.offsets) tiles.scan(a, lane);
+    else tiles.total = static_cast<int>((a.P + BM - 1) / BM);
     const int64_t n = static_cast<int64_t>(tiles.total) * ncol;
     const int64_t first = n * xcd / 8, mine = n * (xcd + 1) / 8 - first;
     if (lin >= mine) return false;
     band_walk<BAND>(first + lin, tiles.total, ncol, rt, ct);
-    t = tiles.find(rt, lane);
+    t = a.offsets ? tiles.find(rt, lane) : dense_tile<BM>(a, rt);
     return true;
 }
 

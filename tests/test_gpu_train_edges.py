@@ -231,3 +231,30 @@ def test_forward_of_long_reductions_and_many_columns(counts, N, R):
     ref = pre.clamp(min=0) + r.double()
     within(y, ref, err + HALF[torch.float32] * (ref.abs() + err), "linear")
     within(z, pre, err + HALF[BF] * (pre.abs() + err), "z")
+
+
+@pytest.mark.parametrize("counts,N,K", [((1,), 65568, 2056), ((3, 0, 1, 9, 4, 0, 2, 5), 9000, 2320),
+                                        ((16,), 66000, 2568), ((2, 0, 7), 32776, 3080)])
+def test_streaming_blocks_of_several_strips(counts, N, K):
+    """More strips of weight rows than blocks: a wave's ring goes on from strip to strip and from
+    group to group; waves of unequal numbers of chunks, a last chunk and strip that are not whole."""
+    P, E = sum(counts), len(counts)
+    say(f"streaming {counts} {N} {K}")
+    off = offsets_of(counts)
+    g = torch.Generator(device=DEV).manual_seed(N)
+    x = torch.randn(P, K, generator=g, device=DEV).to(BF)
+    w = torch.randn(E, N, K, generator=g, device=DEV).mul_(0.1).to(BF)
+    y = moe.grouped_matmul(x, w, off.to(DEV))
+    b, r = torch.randn(N, generator=g, device=DEV), torch.randn(P, N, generator=g, device=DEV).to(BF)
+    lin = moe.linear(x, w[0], b, "relu", r) if E == 1 else None
+    for e in range(E):
+        s = slice(int(off[e]), int(off[e + 1]))
+        if counts[e] == 0:
+            continue
+        a, c = x[s].double(), w[e].double().t()
+        ref, size = a @ c, a.abs() @ c.abs()
+        within(y[s], ref, product_bound(ref, size, K, BF), f"group {e}")
+        if lin is not None:
+            err = (K + 3) * U32 * (size + b.double().abs() + r.double().abs())
+            ref = (ref + b.double()).clamp(min=0) + r.double()
+            within(lin, ref, err + HALF[BF] * (ref.abs() + err), "linear")
