@@ -183,7 +183,7 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -607,12 +607,13 @@ _OUT = (torch.bfloat16, torch.float32)
 # 7 us that a small call takes on the host
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _run(fn, first: torch.Tensor, *args) -> None:
     """fn(*args, stream) with `first`'s device current."""
-    index = first.device.index
-    if index == torch.cuda.current_device():
+    index = first.get_device()
+    if index == _current_device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -622,8 +623,9 @@ def _run(fn, first: torch.Tensor, *args) -> None:
 
 
 def _same_device(first: torch.Tensor, *rest: Optional[torch.Tensor]) -> None:
+    index = first.get_device()
     for t in rest:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"tensors on {first.device} and {t.device}: one device is wanted")
 
 
