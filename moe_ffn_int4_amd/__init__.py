@@ -13,7 +13,11 @@ functions below raises.
     y = forward(x, router_w, router_b, experts, shared, top_k)
     r = route(x, router_w, router_b, top_k)           # routing/dispatch only
 
-Weights live in the tiled layouts the kernels read (see include/moe_int4.h);
+The layer's steps are also there one by one with their gradients, on row-major bf16 weights:
+``permute_rows``, ``grouped_matmul`` (``_dx``, ``_dw``), ``swiglu`` (``_backward``), ``combine``
+(``_backward``), and dense layers, ``linear`` (``linear_dz``, ``linear_dx``, ``linear_dw``).
+
+Weights of ``forward`` live in the tiled layouts the kernels read (see include/moe_int4.h);
 untile_int4 / untile_scales / untile_bf16 convert them back to row-major.
 """
 from __future__ import annotations
