@@ -358,8 +358,10 @@ enum moe_act {
  *                           values in dw with `accumulate` (one rounding of the sum)
  * The output is bf16, or fp32 with out_fp32. Groups may be empty: their dw is
  * zero (or unchanged with accumulate). Rows outside every group are not read,
- * and their rows of y and dx are left as they were. Offsets outside [0, P] are
- * clamped to it and a descending pair is an empty group.
+ * and their rows of y and dx are left as they were. Offsets that leave [0, P]
+ * or descend are the caller's mistake, which the device alone could see: they are
+ * clamped, so that nothing outside the operands is read or written, and which rows
+ * of y, dx and dw are then computed is not specified.
  */
 int moe_grouped_matmul(const uint16_t *x, const uint16_t *w, const int32_t *offsets,
                        int64_t P, int64_t E, int64_t N, int64_t K, void *y,

@@ -258,3 +258,21 @@ def test_streaming_blocks_of_several_strips(counts, N, K):
             err = (K + 3) * U32 * (size + b.double().abs() + r.double().abs())
             ref = (ref + b.double()).clamp(min=0) + r.double()
             within(lin, ref, err + HALF[BF] * (ref.abs() + err), "linear")
+
+
+@pytest.mark.parametrize("P,E,N,K", [(3, 4, 264, 136), (14, 4, 8200, 2056)] + [(P, 4, N, K) for P, _, N, K in KERNELS]
+                         + [(2100, 4, 2600, 200)])
+def test_offsets_out_of_order_stay_inside(P, E, N, K):
+    """Nothing outside the operands is written, and what is written comes from the operands."""
+    say(f"offsets out of order {P} {E} {N} {K}")
+    g = gen(P)
+    off = torch.tensor([0, P, P // 2, 3 * P, -7], dtype=torch.int32, device=DEV)
+    x, w, dy = bf16(g, P, K).to(DEV), bf16(g, E, N, K, scale=0.1).to(DEV), bf16(g, P, N).to(DEV)
+    pad = 4096
+    for what, n, call in [("y", P * N, lambda o: moe.grouped_matmul(x, w, off, out=o.view(P, N))),
+                          ("dx", P * K, lambda o: moe.grouped_matmul_dx(dy, w, off, out=o.view(P, K))),
+                          ("dw", E * N * K, lambda o: moe.grouped_matmul_dw(dy, x, off, out=o.view(E, N, K)))]:
+        buf = torch.full((n + 2 * pad,), 7.0, device=DEV)
+        call(buf[pad:pad + n])
+        assert bool((buf[:pad] == 7).all()) and bool((buf[-pad:] == 7).all()), what
+        assert bool(torch.isfinite(buf).all()), what
