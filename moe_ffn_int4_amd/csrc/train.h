@@ -119,8 +119,8 @@ __device__ __forceinline__ float act_slope(float z, int act) {
 }
 
 // dz = dy * act'(z) (bf16) and db = column sums of the unrounded dz (fp32); act
-// none: db alone. Rows are summed in slices of a fixed size into `partial`
-// [linear_dz_slices(T), N] and the slices in order: no atomics.
+// none: db alone. Rows are summed in slices, whose number is the sizes' alone, into `partial`
+// [linear_dz_slices(T, N), N] and the slices in order: no atomics.
 int64_t linear_dz_slices(int64_t T, int64_t N);
 hipError_t launch_linear_dz(const uint16_t* dy, const uint16_t* z, int act, int64_t T, int64_t N,
                             uint16_t* dz, float* db, float* partial, hipStream_t stream);
