@@ -1,6 +1,6 @@
 // matmul.h -- the products of grouped_matmul, its gradients and linear: operands,
 // tile lookup, LDS staging and fragment reads shared by the kernels of
-// matmul_tile.hip, matmul256.hip and matmul_stream.hip.
+// matmul_tile.hip, matmul256.hip, matmul_split.hip and matmul_stream.hip.
 //
 // One launch computes, for every group e (rows offsets[e] .. offsets[e+1] - 1 of
 // the row operands; one group of P rows when offsets is null):
@@ -237,9 +237,10 @@ __device__ __forceinline__ int row_spread(int r) { return (r >> 1) & 7; }
 // row-major, 2 SIZE bytes a row, its 16-byte pieces XORed by red_spread. A transposing
 // 8-byte read is served 32 lanes at a time: 8 rows (four in a row, twice, 8 apart)
 // of 32 bytes each, which the even XOR values put on 16 different groups of four banks
-// (with rows of 128 bytes the lowest bit of the row does its part).
+// (with rows of 128 and 64 bytes the lowest bits of the row do their part).
 template <int SIZE>
 __device__ __forceinline__ int red_spread(int r) {
+    if (SIZE == 32) return ((r >> 3) & 1) << 1;
     if (SIZE == 64) return (((r >> 3) & 1) << 2) | (r & 2);
     return (((r >> 3) & 1) << 3) | ((r & 3) << 1);
 }
@@ -314,7 +315,7 @@ struct Stager {
 // Reader of one operand's fragments from a tile of SIZE values of m / n.
 template <bool TR, int SIZE>
 struct Reader {
-    static constexpr int kSubs = SIZE == 64 ? 2 : 4;
+    static constexpr int kSubs = SIZE < 128 ? 2 : 4;
     int at[TR ? kSubs : 2];  // byte address, TR: by sub-tile, else by slice s
 
     // row0: the wave's first row (m or n) in the tile, a multiple of 32

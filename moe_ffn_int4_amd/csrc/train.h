@@ -34,6 +34,7 @@ struct MatmulArgs {
 };
 
 hipError_t launch_matmul256(int mode, bool linear, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_matmul_split(int mode, bool linear, const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_matmul_stream(bool linear, const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_matmul(int mode, bool linear, const MatmulArgs& a, hipStream_t stream);
 

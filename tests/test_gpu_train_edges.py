@@ -276,3 +276,39 @@ def test_offsets_out_of_order_stay_inside(P, E, N, K):
         call(buf[pad:pad + n])
         assert bool((buf[:pad] == 7).all()) and bool((buf[-pad:] == 7).all()), what
         assert bool(torch.isfinite(buf).all()), what
+
+
+@pytest.mark.parametrize("counts,N,R", [((30,), 9000, 1032), ((1000,), 552, 1000), ((900, 800), 1000, 776)])
+def test_many_columns_of_long_reductions(counts, N, R):
+    """Outputs of more tiles than one kernel's split takes and fewer than the next needs, each direction."""
+    P, E = sum(counts), len(counts)
+    g = gen(R + N)
+    off = offsets_of(counts)
+    x, w, v, dy = bf16(g, P, R), bf16(g, E, N, R, scale=0.1), bf16(g, E, R, N, scale=0.1), bf16(g, P, N)
+    y = moe.grouped_matmul(x.to(DEV), w.to(DEV), off.to(DEV), out_dtype=torch.float32)
+    dx = moe.grouped_matmul_dx(x.to(DEV), v.to(DEV), off.to(DEV))
+    dw = moe.grouped_matmul_dw(dy.to(DEV), x.to(DEV), off.to(DEV))
+    for e in range(E):
+        s = slice(int(off[e]), int(off[e + 1]))
+        for got, a, b, red, out in ((y[s], x[s].double(), w[e].double().t(), R, torch.float32),
+                                    (dx[s], x[s].double(), v[e].double(), R, BF),
+                                    (dw[e], dy[s].double().t(), x[s].double(), counts[e], BF)):
+            ref, size = a @ b, a.abs() @ b.abs()
+            within(got, ref, product_bound(ref, size, red, out), f"group {e}")
+
+
+@pytest.mark.parametrize("out", OUT, ids=["bf16", "fp32"])
+@pytest.mark.parametrize("P,E,N,K", [(600, 1, 72, 88), (1300, 2, 136, 40), (5000, 1, 8, 8)])
+def test_dw_accumulates_over_long_reductions(P, E, N, K, out):
+    g = gen(P + N)
+    counts = split_counts(P, E, 5)
+    off = offsets_of(counts)
+    dy, x = bf16(g, P, N).to(DEV), bf16(g, P, K).to(DEV)
+    dw = torch.randn(E, N, K, generator=g).to(out).to(DEV)
+    old = dw.double()
+    moe.grouped_matmul_dw(dy, x, off.to(DEV), out=dw, accumulate=True)
+    for e in range(E):
+        s = slice(int(off[e]), int(off[e + 1]))
+        a, b = dy[s].double().t(), x[s].double()
+        ref, size = a @ b + old[e], a.abs() @ b.abs() + old[e].abs()
+        within(dw[e], ref, product_bound(ref, size, counts[e] + 1, out), f"dw[{e}]")
