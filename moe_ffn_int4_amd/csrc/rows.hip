@@ -178,6 +178,63 @@ __global__ __launch_bounds__(NT) void linear_dz_kernel(const uint16_t* dy, const
     }
 }
 
+// Up to 512 rows: all of 64 columns in one block of 16 waves, eight lanes a row, four rows a
+// thread, all loaded at once; the rows of a wave are added across lanes, the waves in order. One
+// launch: 126 x 2968 takes 4.1 us instead of 5.8 in a graph, 9.7 instead of 12 called one by
+// one; 508 x 2104 8.0 (7.7) and 10.0 (12.4). At 1024 rows the arithmetic of so few blocks
+// shows: 13.1 against 4.9 for 64 columns.
+constexpr int kDzWaves = 16;
+constexpr int kDzUnder = 4;
+constexpr int64_t kDzOneLaunch = kDzWaves * 8 * kDzUnder;
+template <int ACT>
+__global__ __launch_bounds__(64 * kDzWaves) void linear_dz_columns_kernel(const uint16_t* dy, const uint16_t* z,
+                                                                          int64_t T, int64_t N, uint16_t* dz,
+                                                                          float* __restrict__ db) {
+    __shared__ float part[kDzWaves * 64];
+    constexpr int kRows = kDzWaves * 8;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x & 7);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r0 = threadIdx.x >> 3;
+    float sum[8] = {};
+    if (c * 8 < N && r0 < T) {
+        float d[kDzUnder][8], v[kDzUnder][8];
+#pragma unroll
+        for (int u = 0; u < kDzUnder; ++u) {
+            // rows past the end load the last one, for nothing: a branch would wait for each load
+            const int64_t r = r0 + u * kRows < T ? r0 + u * kRows : T - 1;
+            load8(dy + r * N + c * 8, d[u]);
+            if (ACT != MOE_ACT_NONE) load8(z + r * N + c * 8, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kDzUnder; ++u) {
+            const int64_t r = r0 + u * kRows;
+            if (r >= T) break;
+            if (ACT != MOE_ACT_NONE) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[u][i] *= act_slope(v[u][i], ACT);
+                save8(dz + r * N + c * 8, d[u]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += d[u][i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int off = 8; off < 64; off <<= 1) sum[i] += __shfl_xor(sum[i], off, kWave);
+    }
+    if (lane < 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[wave * 64 + lane * 8 + i] = sum[i];
+    }
+    __syncthreads();
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
+    if (threadIdx.x >= 64 || col >= N || !db) return;
+    float s = part[threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kDzWaves; ++w) s += part[w * 64 + threadIdx.x];
+    db[col] = s;
+}
+
 // A block adds the slices of 32 columns: eight threads a column take every eighth slice,
 // and their sums are added in order. (One thread a column: 128 loads in a row.)
 __global__ __launch_bounds__(NT) void dz_finish_kernel(const float* __restrict__ partial, int slices, int64_t N,
@@ -211,11 +268,11 @@ static int dz_shift(int64_t N) {
 // Slices of the rows: 64 rows each, shorter ones while there are fewer than kDzBlocks
 // blocks and each thread has a row (gelu, us: 800 x 3032 9.1 against 12.9 in slices of 64,
 // 3655 x 944 10.3 against 15.1; with 128, 256 and 1024 blocks 10.5, 9.5, 10.2 and 12.7, 10.0,
-// 11.7); one, and no second launch, up to eight rows a thread (16 x 1024: 6.0 against 8.1).
+// 11.7). One for what linear_dz_columns_kernel takes.
 int64_t linear_dz_slices(int64_t T, int64_t N) {
     const int shift = dz_shift(N);
     const int64_t cols = (N + (8 << shift) - 1) >> (shift + 3), stride = NT >> shift;
-    if (T <= 8 * stride) return 1;
+    if (T <= kDzOneLaunch) return 1;
     int64_t s = (kDzBlocks + cols - 1) / cols;
     const int64_t most = (T + stride - 1) / stride, least = (T + kDzRows - 1) / kDzRows;
     s = s < most ? s : most;
@@ -226,10 +283,20 @@ int64_t linear_dz_slices(int64_t T, int64_t N) {
 hipError_t launch_linear_dz(const uint16_t* dy, const uint16_t* z, int act, int64_t T, int64_t N,
                             uint16_t* dz, float* db, float* partial, hipStream_t stream) {
     const int64_t slices = linear_dz_slices(T, N);
+    if (slices == 1) {
+        auto* one = act == MOE_ACT_RELU        ? linear_dz_columns_kernel<MOE_ACT_RELU>
+                    : act == MOE_ACT_SILU      ? linear_dz_columns_kernel<MOE_ACT_SILU>
+                    : act == MOE_ACT_GELU      ? linear_dz_columns_kernel<MOE_ACT_GELU>
+                    : act == MOE_ACT_GELU_TANH ? linear_dz_columns_kernel<MOE_ACT_GELU_TANH>
+                                               : linear_dz_columns_kernel<MOE_ACT_NONE>;
+        hipLaunchKernelGGL(one, dim3(static_cast<unsigned>((N + 63) / 64)), dim3(64 * kDzWaves), 0, stream, dy, z, T,
+                           N, dz, db);
+        return hipGetLastError();
+    }
     const int64_t rows = (T + slices - 1) / slices;
     const int shift = dz_shift(N);
     const int64_t cols = (N + (8 << shift) - 1) >> (shift + 3);
-    float* sums = !db ? nullptr : slices == 1 ? db : partial;
+    float* sums = db ? partial : nullptr;
     auto* kernel = act == MOE_ACT_RELU        ? linear_dz_kernel<MOE_ACT_RELU>
                    : act == MOE_ACT_SILU      ? linear_dz_kernel<MOE_ACT_SILU>
                    : act == MOE_ACT_GELU      ? linear_dz_kernel<MOE_ACT_GELU>
@@ -238,7 +305,7 @@ hipError_t launch_linear_dz(const uint16_t* dy, const uint16_t* z, int act, int6
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(cols), static_cast<unsigned>(slices)), dim3(NT), 0,
                        stream, dy, z, T, N, shift, rows, dz, sums);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !db || slices == 1) return e;
+    if (e != hipSuccess || !db) return e;
     hipLaunchKernelGGL(dz_finish_kernel, dim3(static_cast<unsigned>((N + 31) / 32)), dim3(NT), 0, stream,
                        partial, static_cast<int>(slices), N, db);
     return hipGetLastError();

@@ -312,3 +312,34 @@ def test_dw_accumulates_over_long_reductions(P, E, N, K, out):
         a, b = dy[s].double().t(), x[s].double()
         ref, size = a @ b + old[e], a.abs() @ b.abs() + old[e].abs()
         within(dw[e], ref, product_bound(ref, size, counts[e] + 1, out), f"dw[{e}]")
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("T,N", [(511, 72), (512, 8), (513, 72), (512, 1000), (65, 136), (129, 8192), (600, 64)])
+def test_linear_dz_around_its_kernels(T, N, act):
+    """Rows around one launch's; a buffer around dz and db that stays; in place; without db (through C)."""
+    g = gen(T + N)
+    dy, z = bf16(g, T, N), bf16(g, T, N, scale=2.0)
+    zz = z.double()
+    s = torch.sigmoid(zz)
+    slope = s + zz * s * (1 - s) if act == "silu" else torch.ones_like(zz)
+    ref = dy.double() * slope
+    err = 40 * U32 * dy.double().abs() * 1.2
+    pad = 128
+    dbuf = torch.full((N + 2 * pad,), 7.0, device=DEV)
+    zbuf = torch.full((T * N + 2 * pad,), 7.0, dtype=BF, device=DEV)
+    out = zbuf[pad:-pad].view(T, N) if act != "none" else None
+    dz, db = moe.linear_dz(dy.to(DEV), z.to(DEV) if act != "none" else None, act, out=out, db=dbuf[pad:-pad])
+    within(db, ref.sum(0), err.sum(0) + (T + 1) * U32 * ref.abs().sum(0), "db")
+    assert bool((dbuf[:pad] == 7).all()) and bool((dbuf[-pad:] == 7).all())
+    if act == "none":
+        return
+    within(dz, ref, err + HALF[BF] * (ref.abs() + err), "dz")
+    assert bool((zbuf[:pad] == 7).all()) and bool((zbuf[-pad:] == 7).all())
+    a = dy.to(DEV)
+    d2, db2 = moe.linear_dz(a, z.to(DEV), act, out=a)
+    assert torch.equal(d2, dz) and torch.equal(db2, db)
+    a, b, c = dy.to(DEV), z.to(DEV), torch.empty(T, N, dtype=BF, device=DEV)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert moe.lib().moe_linear_dz(a.data_ptr(), b.data_ptr(), moe.ACTS[act], T, N, c.data_ptr(), None, None, 0, stream) == 0
+    assert torch.equal(c, dz)
