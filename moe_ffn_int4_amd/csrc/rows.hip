@@ -360,38 +360,41 @@ __global__ __launch_bounds__(NT) void combine_rows_kernel(const O* __restrict__ 
     save8(y + t * d + c * 8, acc);
 }
 
-// One wave for each (token, j): d_o[slot] = g dy[t] and d_gates[t, j] = <dy[t], o[slot]>.
-template <typename O>
+// d_o[slot] = g dy[t] and d_gates[t, j] = <dy[t], o[slot]>: a wave for each (token, j), or,
+// for rows of up to 256 values, 1 << shift lanes that cover the row. (6221 x 8 x 80: 8.4 against 18.9
+// us with whole waves, 16384 x 8 x 256 36 against 50. As one kernel with runtime lanes,
+// 8192 x 8 x 520 took 42 instead of 34.)
+template <typename O, bool WAVE>
 __global__ __launch_bounds__(NT) void combine_backward_kernel(const uint16_t* __restrict__ dy,
                                                               const O* __restrict__ o,
                                                               const int32_t* __restrict__ inv,
                                                               const float* __restrict__ gates, int64_t T,
-                                                              int top_k, int64_t d,
+                                                              int top_k, int64_t d, int shift_,
                                                               uint16_t* __restrict__ d_o,
                                                               float* __restrict__ d_gates) {
-    const int64_t pair = static_cast<int64_t>(block_index()) * (NT / 64) + (threadIdx.x >> 6);
+    const int shift = WAVE ? 6 : shift_, lanes = 1 << shift, lane = threadIdx.x & (lanes - 1);
+    const int64_t pair = (static_cast<int64_t>(block_index()) << (8 - shift)) + (threadIdx.x >> shift);
     if (pair >= T * top_k) return;
-    const int lane = threadIdx.x & 63;
     const int64_t t = pair / top_k;
     const int slot = inv[pair];
     const bool in = slot >= 0 && slot < T * top_k;
     const float g = gates ? gates[pair] : 1.0f;
     float dot = 0.f;
     const uint16_t* from = dy + t * d;
-    const int64_t pieces = in ? d / 8 : 0;
+    const int64_t row = static_cast<int64_t>(slot) * d, pieces = in ? d / 8 : 0;
     // four pieces of each operand under way at once
-    for (int64_t c0 = lane; c0 < pieces; c0 += 256) {
+    for (int64_t c0 = lane; c0 < pieces; c0 += 4 * lanes) {
         float v[4][8], w[4][8];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int64_t c = c0 + 64 * u;
+            const int64_t c = c0 + u * lanes;
             if (c >= pieces) continue;
             load8(from + c * 8, v[u]);
-            if (d_gates) load8(o + static_cast<int64_t>(slot) * d + c * 8, w[u]);
+            if (d_gates) load8(o + row + c * 8, w[u]);
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int64_t c = c0 + 64 * u;
+            const int64_t c = c0 + u * lanes;
             if (c >= pieces) continue;
             if (d_gates) {
 #pragma unroll
@@ -399,11 +402,13 @@ __global__ __launch_bounds__(NT) void combine_backward_kernel(const uint16_t* __
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[u][i] *= g;
-            save8(d_o + static_cast<int64_t>(slot) * d + c * 8, v[u]);
+            save8(d_o + row + c * 8, v[u]);
         }
     }
     if (!d_gates) return;
-    dot = wave_sum(dot);
+    if (WAVE) dot = wave_sum(dot);
+    else
+        for (int off = lanes >> 1; off > 0; off >>= 1) dot += __shfl_xor(dot, off, kWave);
     if (lane == 0) d_gates[pair] = dot;
 }
 
@@ -433,14 +438,20 @@ hipError_t launch_combine_rows(const void* o, bool o_fp32, const int32_t* inv, c
 hipError_t launch_combine_backward(const uint16_t* dy, const void* o, bool o_fp32, const int32_t* inv,
                                    const float* gates, int64_t T, int top_k, int64_t d, uint16_t* d_o,
                                    float* d_gates, hipStream_t stream) {
-    const int64_t blocks = (T * top_k + NT / 64 - 1) / (NT / 64);
+    int shift = 0;
+    while ((1 << shift) < 64 && (8 << shift) < d) ++shift;
+    const int64_t per = NT >> shift, blocks = (T * top_k + per - 1) / per;
     const dim3 grid = block_grid(blocks);
+    auto launch = [&](auto* kernel, auto* rows) {
+        hipLaunchKernelGGL(kernel, grid, dim3(NT), 0, stream, dy, rows, inv, gates, T, top_k, d, shift, d_o, d_gates);
+    };
+    const auto* o32 = static_cast<const float*>(o);
+    const auto* o16 = static_cast<const uint16_t*>(o);
     if (o_fp32)
-        hipLaunchKernelGGL(combine_backward_kernel<float>, grid, dim3(NT), 0, stream, dy,
-                           static_cast<const float*>(o), inv, gates, T, top_k, d, d_o, d_gates);
+        shift == 6 ? launch(&combine_backward_kernel<float, true>, o32) : launch(&combine_backward_kernel<float, false>, o32);
     else
-        hipLaunchKernelGGL(combine_backward_kernel<uint16_t>, grid, dim3(NT), 0, stream, dy,
-                           static_cast<const uint16_t*>(o), inv, gates, T, top_k, d, d_o, d_gates);
+        shift == 6 ? launch(&combine_backward_kernel<uint16_t, true>, o16)
+                   : launch(&combine_backward_kernel<uint16_t, false>, o16);
     return hipGetLastError();
 }
 

@@ -81,3 +81,18 @@ def test_expert_rows_past_32_bits():
         within(d_o[inv.view(T, k)[s].long()], terms, (HALF[BF] + U32) * 1.01 * terms.abs(), "d_o")
         dot = (x[s].double() ** 2).sum(1, keepdim=True).expand(-1, k)
         within(dg[s], dot, (d + 1) * U32 * dot, "d_gates")
+
+
+def test_more_waves_of_pairs_than_a_grid_row():
+    T, k, d = (1 << 21) + 3, 8, 264
+    say(f"combine_backward of {T * k} pairs of {d}")
+    dy, gates = _rand(T, d), torch.rand(T, k, device=DEV)
+    inv = torch.arange(T * k, dtype=torch.int32, device=DEV).view(T, k)
+    o = _rand(T * k, d)
+    d_o = torch.full((T * k, d), 7.0, dtype=BF, device=DEV)
+    _, dg = moe.combine_backward(dy, o, inv, gates, out=d_o)
+    for s in (slice(0, 1000), slice(T // 2, T // 2 + 1000), slice(T - 1000, T)):
+        want = (gates[s].unsqueeze(2) * dy[s].float().unsqueeze(1)).to(BF)
+        assert torch.equal(d_o.view(T, k, d)[s], want)
+        prod = dy[s].double().unsqueeze(1) * o.view(T, k, d)[s].double()
+        within(dg[s], prod.sum(2), (d + 1) * U32 * prod.abs().sum(2), "d_gates")
