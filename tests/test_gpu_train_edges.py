@@ -343,3 +343,61 @@ def test_linear_dz_around_its_kernels(T, N, act):
     stream = torch.cuda.current_stream().cuda_stream
     assert moe.lib().moe_linear_dz(a.data_ptr(), b.data_ptr(), moe.ACTS[act], T, N, c.data_ptr(), None, None, 0, stream) == 0
     assert torch.equal(c, dz)
+
+
+def test_calls_from_several_threads():
+    """Four threads, each with a stream of its own, call every operator at once; one of
+    them also makes calls that are refused, whose text the others do not see."""
+    import threading
+    T, k, d, h, E = 96, 2, 264, 136, 4
+    g = gen(12)
+    perm = torch.randperm(T * k, generator=g).to(torch.int32)
+    inv = torch.empty_like(perm)
+    inv[perm.long()] = torch.arange(T * k, dtype=torch.int32)
+    off = offsets_of(split_counts(T * k, E, 3)).to(DEV)
+    perm, inv = perm.to(DEV), inv.view(T, k).to(DEV)
+    x, gates = bf16(g, T, d).to(DEV), torch.rand(T, k, generator=g).to(DEV)
+    w13, w2 = bf16(g, E, 2 * h, d, scale=0.1).to(DEV), bf16(g, E, d, h, scale=0.1).to(DEV)
+    s1, b1 = bf16(g, h, d, scale=0.1).to(DEV), torch.randn(h, generator=g).to(DEV)
+
+    def run():
+        xp = moe.permute_rows(x, perm, k)
+        z = moe.grouped_matmul(xp, w13, off)
+        hid = moe.swiglu(z)
+        o = moe.grouped_matmul(hid, w2, off)
+        y = moe.combine(o, inv, gates, residual=x)
+        d_o, dg = moe.combine_backward(y, o, inv, gates)
+        dz = moe.swiglu_backward(moe.grouped_matmul_dx(d_o, w2, off), z)
+        pre = torch.empty(T, h, dtype=BF, device=DEV)
+        a = moe.linear(x, s1, b1, "gelu", z=pre)
+        da, db = moe.linear_dz(a, pre, "gelu")
+        return [xp, z, hid, o, y, d_o, dg, dz, a, da, db, moe.grouped_matmul_dw(d_o, hid, off),
+                moe.grouped_matmul_dw(dz, xp, off, out_dtype=torch.float32), moe.linear_dx(da, s1), moe.linear_dw(da, x)]
+
+    want = run()
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for rep in range(5):
+                    got[i, rep] = run()
+                    if i == 0:
+                        with pytest.raises(moe.MoEError, match="overlaps"):
+                            moe.swiglu(want[1], out=want[1].view(-1)[:T * k * h].view(T * k, h))
+                torch.cuda.current_stream().synchronize()
+        except BaseException as e:  # noqa: B036 -- shown by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    torch.cuda.synchronize()
+    assert len(got) == 20
+    for outs in got.values():
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
