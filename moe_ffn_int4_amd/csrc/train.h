@@ -7,14 +7,10 @@
 #include <stdint.h>
 
 #include "kernels.h"
+#include "matmul_rule.h"
 #include "moe_int4.h"
 
 namespace moe {
-
-// products of matmul.h
-constexpr int kFwd = 0;
-constexpr int kDx = 1;
-constexpr int kDw = 2;
 
 struct MatmulArgs {
     const uint16_t* a;       // kFwd: x [P, K]; kDx, kDw: dy [P, N]
