@@ -179,7 +179,8 @@ template <int MODE, int BM, int BN, int BAND>
 __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int lane, MatTile& t, int& rt, int& ct) {
     const int ncol = static_cast<int>(((MODE == kFwd ? a.N : a.K) + BN - 1) / BN);
     const int xcd = blockIdx.x & 7;
-    int64_t lin = blockIdx.x >> 3;
+    // a grid of several rows has kGridX blocks in each
+    int64_t lin = (blockIdx.x >> 3) + blockIdx.y * (kGridX >> 3);
     if (MODE == kDw) {
         const int nrow = static_cast<int>((a.N + BM - 1) / BM);
         const int64_t n = static_cast<int64_t>(nrow) * ncol;

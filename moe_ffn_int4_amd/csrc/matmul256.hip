@@ -507,7 +507,7 @@ static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     // against 1554 us (forward 1301 against 1304).
     int64_t blocks = matmul256_blocks<MODE>(a);
     if ((MODE == kDw || a.E == 1) && blocks > 256) blocks = 256;
-    if (blocks > kGridX) return hipErrorInvalidConfiguration;
+    if (blocks > kGridX) blocks = kGridX;  // of several tiles each
     hipLaunchKernelGGL((matmul256_kernel<MODE, LINEAR>), dim3(static_cast<unsigned>(blocks)),
                        dim3(64 * kWaves), kStages + kTable, stream, a);
     return hipGetLastError();

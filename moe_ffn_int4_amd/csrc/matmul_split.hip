@@ -105,9 +105,7 @@ static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
         reinterpret_cast<const void*>(&matmul_split_kernel<MODE, LINEAR>),
         hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (ready != hipSuccess) return ready;
-    const int64_t blocks = matmul_blocks<MODE, T, T>(a);
-    if (blocks > kGridX) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((matmul_split_kernel<MODE, LINEAR>), dim3(static_cast<unsigned>(blocks)),
+    hipLaunchKernelGGL((matmul_split_kernel<MODE, LINEAR>), block_grid(matmul_blocks<MODE, T, T>(a)),
                        dim3(64 * kWaves), kLds, stream, a);
     return hipGetLastError();
 }

@@ -134,9 +134,7 @@ static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
         reinterpret_cast<const void*>(&matmul_tile_kernel<MODE, LINEAR, T, RING, KS>),
         hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (ready != hipSuccess) return ready;
-    const int64_t blocks = matmul_blocks<MODE, T, T>(a);
-    if (blocks > 2 * kGridX) return hipErrorInvalidConfiguration;  // 256 threads each
-    hipLaunchKernelGGL((matmul_tile_kernel<MODE, LINEAR, T, RING, KS>), dim3(static_cast<unsigned>(blocks)),
+    hipLaunchKernelGGL((matmul_tile_kernel<MODE, LINEAR, T, RING, KS>), block_grid(matmul_blocks<MODE, T, T>(a)),
                        dim3(64 * kWaves * KS), kLds, stream, a);
     return hipGetLastError();
 }
