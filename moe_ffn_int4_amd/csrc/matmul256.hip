@@ -496,10 +496,10 @@ static int64_t matmul256_blocks(const MatmulArgs& a) {
 
 template <int MODE, bool LINEAR>
 static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
-    static const hipError_t ready = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(&matmul256_kernel<MODE, LINEAR>),
-        hipFuncAttributeMaxDynamicSharedMemorySize, kStages + kTable);
-    if (ready != hipSuccess) return ready;
+    static LdsDevices allowed;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(&matmul256_kernel<MODE, LINEAR>),
+                                   kStages + kTable, allowed);
+    if (e != hipSuccess) return e;
     // Persistent blocks, one a CU, where the tiles cost about the same (a dense
     // product) or are short (weight gradients): 16 experts of 512 rows, 5120 x 8192,
     // 822 us against 886 with a block a tile. Tiles of ragged groups differ in cost,

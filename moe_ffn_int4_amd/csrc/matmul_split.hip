@@ -101,10 +101,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_split_kernel(MatmulArgs
 
 template <int MODE, bool LINEAR>
 static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
-    static const hipError_t ready = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(&matmul_split_kernel<MODE, LINEAR>),
-        hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-    if (ready != hipSuccess) return ready;
+    static LdsDevices allowed;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(&matmul_split_kernel<MODE, LINEAR>), kLds, allowed);
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL((matmul_split_kernel<MODE, LINEAR>), block_grid(matmul_blocks<MODE, T, T>(a)),
                        dim3(64 * kWaves), kLds, stream, a);
     return hipGetLastError();

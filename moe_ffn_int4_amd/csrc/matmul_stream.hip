@@ -191,10 +191,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_stream_kernel(MatmulArg
 
 template <typename S, bool LINEAR>
 static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
-    static const hipError_t ready = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(&matmul_stream_kernel<S, LINEAR>),
-        hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
-    if (ready != hipSuccess) return ready;
+    static LdsDevices allowed;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(&matmul_stream_kernel<S, LINEAR>), S::kLds, allowed);
+    if (e != hipSuccess) return e;
     const int64_t partial = a.E < a.P ? a.E : a.P;
     const int64_t strips = (a.P / S::MX + partial) * ((a.N + kRowsN - 1) / kRowsN);
     const int blocks = static_cast<int>(strips < kMostBlocks ? strips : kMostBlocks);

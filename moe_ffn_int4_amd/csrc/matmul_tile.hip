@@ -130,10 +130,10 @@ __global__ __launch_bounds__(64 * kWaves * KS, KS == 1 ? 2 : KS) void matmul_til
 template <int MODE, bool LINEAR, int T, int RING, int KS>
 static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     constexpr int kLds = KS * RING * 2 * T * kStepR * 2;
-    static const hipError_t ready = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(&matmul_tile_kernel<MODE, LINEAR, T, RING, KS>),
-        hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-    if (ready != hipSuccess) return ready;
+    static LdsDevices allowed;
+    const hipError_t e = allow_lds(
+        reinterpret_cast<const void*>(&matmul_tile_kernel<MODE, LINEAR, T, RING, KS>), kLds, allowed);
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL((matmul_tile_kernel<MODE, LINEAR, T, RING, KS>), block_grid(matmul_blocks<MODE, T, T>(a)),
                        dim3(64 * kWaves * KS), kLds, stream, a);
     return hipGetLastError();

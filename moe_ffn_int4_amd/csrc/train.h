@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "kernels.h"
+#include "lds_limit.h"
 #include "matmul_rule.h"
 #include "moe_int4.h"
 
