@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "gemm_common.h"
+#include "lds_limit.h"
 
 namespace moe {
 
@@ -508,9 +509,9 @@ static constexpr size_t kGemm256LdsFp8 = NFSTAGE2 * FSTAGE2;
 template <bool UP, bool F8>
 static hipError_t launch256(const GroupedGemmArgs& a, unsigned ncol, hipStream_t stream) {
     constexpr size_t lds = F8 ? kGemm256LdsFp8 : kGemm256Lds;
-    static hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(&grouped_gemm256_kernel<UP, F8>),
-        hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
+    static LdsDevices allowed;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(&grouped_gemm256_kernel<UP, F8>),
+                                   static_cast<int>(lds), allowed);
     if (e != hipSuccess) return e;
     dim3 grid(xcd_grid(static_cast<int64_t>(max_row_tiles256(a)) * ncol, tile_weight(a)));
     MOE_LAUNCH((grouped_gemm256_kernel<UP, F8>), grid, dim3(NT2), lds, stream, a);

@@ -46,8 +46,39 @@ CASES = ["fwd,1,1,8192,5120", "fwd,4,4,8192,5120",           # streaming, four r
          "fwd,512,1,8192,5120", "fwd,500,2,8192,5120", "dx,512,1,5120,8192", "dw,700,1,1608,1736",  # of 128, four stages
          "fwd,2100,1,2904,2904", "fwd,2100,4,2904,2904", "dx,2100,4,2904,2904", "dw,2100,4,2904,2904"]  # of 256
 
+FORWARD = r"""
+import ctypes, sys
+stub = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)
+L = ctypes.CDLL(sys.argv[2])
+P, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+class Dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("T", "d", "E", "h")] + [("top_k", i32), ("group_size", i32)]
+class Int4(ctypes.Structure):
+    _fields_ = [("p", P * 6)]
+class Fp8(ctypes.Structure):
+    _fields_ = [("p", P * 6), ("act_ub", ctypes.c_float)]
+class Shared(ctypes.Structure):
+    _fields_ = [("p", P * 3)]
+for fn in (L.moe_forward_path, L.moe_forward_fp8):
+    fn.argtypes = [P, P, P, P, P, P, P, P, P, i32, P, sz, P]
+L.moe_last_error.restype = ctypes.c_char_p
+at = [0x10000000000 + i * (1 << 42) for i in range(16)]
+dims = Dims(2048, 512, 4, 512, 1, 128)
+int4, fp8, shared = Int4((P * 6)(*at[:6])), Fp8((P * 6)(*at[:6]), 0.0), Shared((P * 3)(*at[6:9]))
+for device in (0, 1, 63, 0):
+    stub.stub_set_device(device)
+    for fn, experts in ((L.moe_forward_path, int4), (L.moe_forward_fp8, fp8)):
+        st = fn(ctypes.byref(dims), at[9], at[10], None, ctypes.byref(experts), ctypes.byref(shared), at[11], None, None,
+                4, at[12], 1 << 40, None)
+        assert st == 0, (st, L.moe_last_error())
+out = (ctypes.c_int * 3)()
+stub.stub_counts(out)
+print(*out)
+"""
 
-def test_every_device_allows_the_kernels_their_lds(tmp_path):
+
+def _run(tmp_path, child, *args):
+    """(launches, those of more than 64 KB, those past what their device allows) of `child`."""
     if not os.path.exists(moe.LIB_PATH):
         from moe_ffn_int4_amd import build
         build.build()
@@ -57,8 +88,19 @@ def test_every_device_allows_the_kernels_their_lds(tmp_path):
     stub = str(tmp_path / "libstub.so")
     subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(rocm, "include"),
                     "-Wno-attributes", "-o", stub, os.path.join(ROOT, "tests", "hip_calls_stub.cpp")], check=True)
-    r = subprocess.run([sys.executable, "-c", CHILD, stub, moe.LIB_PATH, *CASES], capture_output=True, text=True)
+    r = subprocess.run([sys.executable, "-c", child, stub, moe.LIB_PATH, *args], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout + r.stderr
-    launches, large, refused = map(int, r.stdout.split())
+    return map(int, r.stdout.split())
+
+
+def test_every_device_allows_the_kernels_their_lds(tmp_path):
+    launches, large, refused = _run(tmp_path, CHILD, *CASES)
     assert launches == large == 4 * len(CASES), (launches, large)
+    assert refused == 0, f"{refused} of {large} launches ask for more LDS than their device allows the kernel"
+
+
+def test_every_device_allows_the_layer_its_lds(tmp_path):
+    """The layer's forward in tiles of 256: int4 and fp8 experts, up and down projections."""
+    launches, large, refused = _run(tmp_path, FORWARD)
+    assert launches > large >= 4 * 4, (launches, large)
     assert refused == 0, f"{refused} of {large} launches ask for more LDS than their device allows the kernel"
