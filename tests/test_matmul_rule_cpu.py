@@ -4,6 +4,8 @@ import subprocess
 
 import pytest
 
+import matmul_cases
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "moe_ffn_int4_amd", "csrc")
 MODES = {"fwd": 0, "dx": 1, "dw": 2}
@@ -39,3 +41,14 @@ def rule(tmp_path_factory):
 ])
 def test_groups_shorter_than_a_tile(rule, way, P, E, N, K, kernel):
     assert rule((way, P, E, N, K)) == [kernel]
+
+
+def test_cases_of_each_kernel(rule):
+    """What the GPU tests call a kernel's sizes are the sizes that the rule sends to it."""
+    for kernel, cases in matmul_cases.GROUPED.items():
+        for way, counts, N, K in cases:
+            P = sum(counts) + matmul_cases.LEAD + matmul_cases.TAIL
+            assert rule((way, P, len(counts), N, K)) == [kernel], (way, counts, N, K)
+    for kernel, cases in matmul_cases.LINEAR.items():
+        for T, N, K in cases:
+            assert rule(("fwd", T, 1, N, K)) == [kernel], (T, N, K)
