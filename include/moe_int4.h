@@ -335,7 +335,14 @@ int moe_route(const moe_dims *dims, const uint16_t *x, const float *router_w,
  * different streams, and captured graphs of them, share no memory.
  */
 
-/* Activations of moe_linear / moe_linear_dz. */
+/*
+ * Activations of moe_linear / moe_linear_dz. They, their slopes and SwiGLU's are
+ * evaluated in fp32, before the one rounding of an output: to 2^-19 + |e| 2^-21 of
+ * the value (of the larger term, where a slope is a sum of two), e being the exponent
+ * in it: z (silu), z^2 / 2 (gelu, whose Phi is a fitted polynomial times exp(-z^2 / 2)),
+ * sqrt(8/pi) (z + 0.044715 z^3) (gelu_tanh). Magnitudes below 2^-119 may come out as 0.
+ * Past +-90 a slope is its limit, also at infinities.
+ */
 enum moe_act {
     MOE_ACT_NONE = 0,
     MOE_ACT_RELU = 1,
