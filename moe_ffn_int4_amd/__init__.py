@@ -16,6 +16,9 @@ functions below raises.
 The layer's steps are also there one by one with their gradients, on row-major bf16 weights:
 ``permute_rows``, ``grouped_matmul`` (``_dx``, ``_dw``), ``swiglu`` (``_backward``), ``combine``
 (``_backward``), and dense layers, ``linear`` (``linear_dz``, ``linear_dx``, ``linear_dw``).
+They take no part in torch's autograd: results carry no graph, also where an argument requires
+gradients, and a program calls the gradients' functions itself (or in its own
+``torch.autograd.Function``).
 
 Weights of ``forward`` live in the tiled layouts the kernels read (see include/moe_int4.h);
 untile_int4 / untile_scales / untile_bf16 convert them back to row-major.
@@ -601,7 +604,7 @@ def route(x: torch.Tensor, router_w: torch.Tensor, router_b: Optional[torch.Tens
 #
 # The layer's products one by one, with their gradients. They run on the current
 # stream of their first argument's device, which need not be the current device; all
-# tensors must be on it.
+# tensors must be on it. None is differentiated by torch's autograd.
 
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _OUT = (torch.bfloat16, torch.float32)
