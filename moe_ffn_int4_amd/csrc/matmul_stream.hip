@@ -203,6 +203,9 @@ static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// The shape goes by the mean group, the sizes being unknown here. A group of more rows than MX
+// streams its weights once for each MX of them: 512 rows over E = 128, 16384 x 5120, take 3.5 ms in
+// groups of four, 2.9 with all rows in one group (tiles of 128 then: 0.11).
 hipError_t launch_matmul_stream(bool linear, const MatmulArgs& a, hipStream_t stream) {
     using Few = StreamShape<4, 256, 2>;
     using Many = StreamShape<16, 128, 2>;

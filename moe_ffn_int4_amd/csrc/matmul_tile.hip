@@ -69,7 +69,8 @@ __global__ __launch_bounds__(64 * kWaves * KS, KS == 1 ? 2 : KS) void matmul_til
     const uint32_t at = lds_address(ring);
     constexpr int kLoads = 2 * T / 8 / kWaves;  // a wave's, a step
     // A's first 32 rows alone where the tile has no more (a wave's first load of two; what LDS
-    // holds of the others goes into rows that are not stored): 17 x 16384 x 5120 dx 53.7 -> 51.4 us
+    // holds of the others goes into rows that are not stored): dx of 30 rows, 16384 x 10240, 93.4 ->
+    // 91.9 us, of 17, 2048 x 16384, 14.7 -> 14.5
     const bool half = MODE != kDw && T == 64 && o.rows <= 32;
     auto request = [&](int stage, int k) __attribute__((always_inline)) {
         if (half) sa.template load<0, T / 64>(at + stage * kStage, part + k * KS, o.red);
