@@ -442,6 +442,53 @@ int moe_combine_backward(const uint16_t *dy, const void *o, int32_t o_fp32,
                          int64_t d, uint16_t *d_o, float *d_gates, void *stream);
 
 /*
+ * One AdamW step over many tensors at once, in place, in fp32:
+ *   g = grad * grad_scale            m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ * p is `master` where it is given, and param is then p rounded; else param itself is read. Products
+ * and sums are rounded one by one (no fused multiply-add), except that 1 / sqrt(1 - beta2^step) is a factor.
+ *
+ * bits 32: m and v are fp32 [n]. bits 8: m and v hold OCP E4M3 codes of m and of sqrt(v) in
+ * blocks of MOE_ADAMW_BLOCK elements with a scale each,
+ *   most = max(max|x|, 2^-100),   scale = most / 448,   code = fp8_rne(x * (448 * (1 / most))),
+ * the last block filled up with zeros: m and v have ceil(n / 128) * 128 bytes, m_scale and v_scale
+ * ceil(n / 128) floats. The update takes the moments before they are rounded to codes. All
+ * codes and scales 0 are a first step's moments. Rounding is to nearest: a decay of v by less
+ * than half a step of its code (of up to 1/16 of sqrt(v)) is lost unless the block's largest
+ * element decays with it, so beta2 near 1 forgets more slowly than in 32 bits.
+ *
+ * Types may differ from tensor to tensor. n >= 0; together at most 2^34 elements. param and grad
+ * are aligned to their type (16 bytes is faster), all else to 16 bytes. What is written (param,
+ * master, m, v and scales of every tensor) must not overlap itself or any gradient
+ * (MOE_ERR_INVALID_ARG), so a tensor cannot be named twice. A NaN or infinite gradient leaves
+ * that element's parameter and moments NaN or infinite (8 bits: an infinite one its whole block's
+ * moments). Launches: one for each 52 tensors. No workspace; the tensors' addresses are copied
+ * at the call, so that a captured graph steps those tensors again.
+ */
+#define MOE_ADAMW_BLOCK 128
+typedef struct moe_adamw_tensor {
+    void *param;        /* bf16 [n], or fp32 with param_fp32 */
+    const void *grad;   /* bf16 [n], or fp32 with grad_fp32 */
+    float *master;      /* fp32 [n], or NULL */
+    void *m, *v;
+    float *m_scale, *v_scale; /* bits 8 alone, else NULL */
+    int64_t n;
+    int32_t param_fp32, grad_fp32;
+} moe_adamw_tensor;
+
+typedef struct moe_adamw_hyper {
+    double lr, beta1, beta2, eps, weight_decay; /* finite; betas in [0, 1), the rest >= 0 */
+    int64_t step;               /* this step's number, 1 for the first; not read with step_device */
+    const int32_t *step_device; /* the number on the device, or NULL */
+    const float *lr_device;     /* lr on the device (lr is then not read), or NULL */
+    const float *grad_scale;    /* on the device, or NULL for 1 */
+} moe_adamw_hyper;
+
+int moe_adamw(const moe_adamw_tensor *tensors, int32_t count, const moe_adamw_hyper *hyper,
+              int32_t bits, void *stream);
+
+/*
  * Per-stage timing for benchmarks (not part of the layer's arithmetic).
  * While enabled, each stage of every moe_forward / moe_route call (and each
  * int4 quantizer call, as MOE_STAGE_QUANTIZE) is timed by

@@ -72,6 +72,13 @@ class _ExpertsFp8(ctypes.Structure):
                 ("act_ub", ctypes.c_float)]
 
 
+class _AdamWHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("step_device", ctypes.c_void_p), ("lr_device", ctypes.c_void_p),
+                ("grad_scale", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -154,6 +161,8 @@ def lib() -> ctypes.CDLL:
         L.moe_combine.restype = ctypes.c_int
         L.moe_combine_backward.argtypes = [P, P, i32, P, P, i64, i32, i64, P, P, P]
         L.moe_combine_backward.restype = ctypes.c_int
+        L.moe_adamw.argtypes = [P, i32, ctypes.POINTER(_AdamWHyper), i32, P]
+        L.moe_adamw.restype = ctypes.c_int
         L.moe_profile_enable.argtypes = [ctypes.c_int]
         L.moe_profile_enable.restype = ctypes.c_int
         L.moe_profile_read.argtypes = [P, P, ctypes.c_int]
@@ -923,6 +932,147 @@ def combine_backward(dy: torch.Tensor, o: torch.Tensor, inv: torch.Tensor, gates
     _run(lib().moe_combine_backward, dy, dy.data_ptr(), o.data_ptr(), o.dtype == torch.float32,
          inv.data_ptr(), gates.data_ptr(), T, top_k, d, d_o.data_ptr(), d_gates.data_ptr())
     return d_o, d_gates
+
+
+# ---------------------------------------------------------------- optimizer step
+
+ADAMW_BLOCK = 128  # elements that share a scale of an 8-bit moment
+_ADAMW_WORDS = 9   # of 8 bytes: a moe_adamw_tensor
+
+
+@dataclass
+class AdamWState:
+    """What ``adamw`` keeps between steps for a list of parameters.
+
+    The moments of all parameters stand in one tensor each, parameter i's from ``starts()[i]``,
+    a multiple of 128; what lies between them is zero and stays so. In 32 bits ``m`` and ``v`` are
+    fp32 [total]. In 8 bits they are uint8 [total], E4M3 codes of m and of sqrt(v), with fp32 scales
+    [total / 128]. ``master``, if there, holds the fp32 copies of bf16 parameters in the same places,
+    which a step updates and rounds to the parameters (what stands at an fp32 parameter's place is not used)."""
+
+    params: list  # bf16 or fp32 tensors of any shape, contiguous, updated in place
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+    master: Optional[torch.Tensor] = None
+
+    @staticmethod
+    def zeros(params, bits: int = 32, master: bool = True) -> "AdamWState":
+        """State before the first step. ``bits``: of a moment, 32 or 8. ``master``: keep fp32
+        copies of bf16 parameters (without, a step smaller than half a bf16 step is lost)."""
+        if bits not in (8, 32):
+            raise ValueError(f"bits = {bits}: 8 or 32")
+        params = list(params)
+        if not params:
+            raise ValueError("no parameters")
+        total, dev = _adamw_starts(params)[-1], params[0].device
+        moment = torch.uint8 if bits == 8 else torch.float32
+        m, v = (torch.zeros(total, dtype=moment, device=dev) for _ in range(2))
+        scales = [torch.zeros(total // ADAMW_BLOCK, dtype=torch.float32, device=dev) if bits == 8 else None
+                  for _ in range(2)]
+        state = AdamWState(params, m, v, *scales)
+        if master and any(p.dtype == torch.bfloat16 for p in params):
+            state.master = torch.zeros(total, dtype=torch.float32, device=dev)
+            for p, at in zip(params, state.starts()):
+                state.master[at:at + p.numel()].copy_(p.detach().reshape(-1))
+        return state
+
+    def starts(self) -> list:
+        """Where each parameter's elements begin in the moments, and the total."""
+        return _adamw_starts(self.params)
+
+    def moments(self, i: int):
+        """(m, v) of parameter i, fp32 in its shape."""
+        p, at = self.params[i], self.starts()[i]
+        n = p.numel()
+        if self.m.dtype != torch.uint8:
+            return tuple(t[at:at + n].reshape(p.shape).clone() for t in (self.m, self.v))
+        end = self.starts()[i + 1]
+        out = []
+        for codes, scale in ((self.m, self.m_scale), (self.v, self.v_scale)):
+            x = codes[at:end].view(torch.float8_e4m3fn).float().reshape(-1, ADAMW_BLOCK)
+            x = x * scale[at // ADAMW_BLOCK:end // ADAMW_BLOCK].unsqueeze(1)
+            out.append(x.reshape(-1)[:n].reshape(p.shape))
+        return out[0], out[1] * out[1]
+
+
+def _adamw_starts(params) -> list:
+    at = [0]
+    for p in params:
+        at.append(at[-1] + (p.numel() + ADAMW_BLOCK - 1) // ADAMW_BLOCK * ADAMW_BLOCK)
+    return at
+
+
+def _device_scalar(t: torch.Tensor, name: str, dtype) -> int:
+    _need(t, name, dtype)
+    if t.numel() != 1:
+        raise ValueError(f"{name} must have one element")
+    return t.data_ptr()
+
+
+def adamw(state: AdamWState, grads, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
+          weight_decay: float = 0.01, grad_scale: Optional[torch.Tensor] = None) -> None:
+    """One AdamW step of all of ``state.params``, in place, in a launch for each 52 of them.
+
+    ``grads``: a bf16 or fp32 tensor for each parameter, or None for one that is left alone.
+    ``step``: this step's number, 1 for the first, and ``lr``: numbers, or tensors of one element
+    on the GPU (int32, fp32), which a captured graph reads anew at each replay. ``grad_scale``
+    (fp32, one element on the GPU) multiplies the gradients: a clipping factor. Updates are
+    made behind torch's back: a parameter's version counter does not move."""
+    params, grads = state.params, list(grads)
+    if len(grads) != len(params):
+        raise ValueError(f"{len(grads)} gradients for {len(params)} parameters")
+    if not params:
+        return
+    m, v, bits = state.m, state.v, 8 if state.m.dtype == torch.uint8 else 32
+    moment = torch.uint8 if bits == 8 else torch.float32
+    first = params[0]
+    index = first.get_device()
+    words, at = [], 0
+    base_m, base_v, base_p = m.data_ptr(), v.data_ptr(), _ptr(state.master)
+    width = 1 if bits == 8 else 4
+    scale_m, scale_v = (_ptr(state.m_scale) or 0, _ptr(state.v_scale) or 0) if bits == 8 else (0, 0)
+    half = torch.bfloat16
+    for i, (p, g) in enumerate(zip(params, grads)):
+        if p.dtype not in _OUT or not p.is_contiguous() or p.get_device() != index or index < 0:
+            raise ValueError(f"parameter {i} must be bf16 or fp32, contiguous, and on the first one's GPU")
+        n, start = p.numel(), at
+        at += (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK * ADAMW_BLOCK
+        if g is None:
+            continue
+        if g.dtype not in _OUT or not g.is_contiguous() or g.get_device() != index or g.shape != p.shape:
+            raise ValueError(f"gradient {i} must be bf16 or fp32, contiguous, of its parameter's shape and on its GPU")
+        p32, g32 = p.dtype is not half, g.dtype is not half
+        words += (p.data_ptr(), g.data_ptr(), 0 if p32 or base_p is None else base_p + 4 * start,
+                  base_m + width * start, base_v + width * start,
+                  scale_m and scale_m + start // ADAMW_BLOCK * 4, scale_v and scale_v + start // ADAMW_BLOCK * 4,
+                  n, int(p32) | int(g32) << 32)
+    _need(m, "m", moment, (at,))
+    _need(v, "v", moment, (at,))
+    scales = (at // ADAMW_BLOCK,)
+    for t, name in ((state.m_scale, "m_scale"), (state.v_scale, "v_scale")):
+        if bits == 8:
+            _need(t, name, torch.float32, scales)
+        elif t is not None:
+            raise ValueError(f"{name} with moments of 32 bits")
+    if state.master is not None:
+        _need(state.master, "master", torch.float32, (at,))
+    h = _AdamWHyper(0.0, float(betas[0]), float(betas[1]), float(eps), float(weight_decay), 0)
+    if isinstance(step, torch.Tensor):
+        h.step_device = _device_scalar(step, "step", torch.int32)
+    else:
+        h.step = int(step)
+    if isinstance(lr, torch.Tensor):
+        h.lr_device = _device_scalar(lr, "lr", torch.float32)
+    else:
+        h.lr = float(lr)
+    if grad_scale is not None:
+        h.grad_scale = _device_scalar(grad_scale, "grad_scale", torch.float32)
+    _same_device(first, m, v, state.m_scale, state.v_scale, state.master, grad_scale,
+                 step if isinstance(step, torch.Tensor) else None, lr if isinstance(lr, torch.Tensor) else None)
+    _run(lib().moe_adamw, first, (ctypes.c_uint64 * max(len(words), 1))(*words), len(words) // _ADAMW_WORDS,
+         ctypes.byref(h), bits)
 
 
 def untile_int4(q: torch.Tensor, rows: int, K: int) -> torch.Tensor:

@@ -3,6 +3,12 @@
 // every check is plain host code that runs before any HIP call.
 #include "train.h"
 
+#include <algorithm>
+#include <cmath>
+#include <memory>
+#include <new>
+
+#include "adamw.h"
 #include "host.h"
 
 namespace {
@@ -339,6 +345,100 @@ int moe_combine_backward(const uint16_t* dy, const void* o, int32_t o_fp32, cons
     HIP_CHECK(moe::launch_combine_backward(dy, o, o_fp32 != 0, inv, gates, T, top_k, d, d_o, d_gates,
                                            static_cast<hipStream_t>(stream)),
               "combine_backward launch");
+    return MOE_OK;
+}
+
+// What a step writes must be apart from itself and from every gradient: the spans sorted
+// by address, where each need only be apart from those that start before it ends.
+static int check_adamw_apart(const moe_adamw_tensor* tensors, int32_t count, int32_t bits) {
+    struct Region {
+        uintptr_t from, to;
+        const char* name;  // null: read alone
+        int32_t tensor;
+    };
+    std::unique_ptr<Region[]> all(new (std::nothrow) Region[static_cast<size_t>(count) * 7]);
+    if (!all) return fail(MOE_ERR_INVALID_ARG, "count = %d: no memory for its checks", count);
+    size_t n = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        const moe_adamw_tensor& t = tensors[i];
+        if (t.n == 0) continue;
+        const int64_t blocks = (t.n + MOE_ADAMW_BLOCK - 1) / MOE_ADAMW_BLOCK;
+        const int64_t moment = bits == 8 ? blocks * MOE_ADAMW_BLOCK : t.n * 4;
+        auto add = [&](const void* p, int64_t bytes, const char* name) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+            if (p) all[n++] = Region{a, a + static_cast<uintptr_t>(bytes), name, i};
+        };
+        add(t.grad, t.n * (t.grad_fp32 ? 4 : 2), nullptr);
+        add(t.param, t.n * (t.param_fp32 ? 4 : 2), "param");
+        add(t.master, t.n * 4, "master");
+        add(t.m, moment, "m");
+        add(t.v, moment, "v");
+        if (bits == 8) {
+            add(t.m_scale, blocks * 4, "m_scale");
+            add(t.v_scale, blocks * 4, "v_scale");
+        }
+    }
+    std::sort(all.get(), all.get() + n, [](const Region& a, const Region& b) { return a.from < b.from; });
+    const Region *written = nullptr, *read = nullptr;  // those that reach furthest so far
+    for (size_t k = 0; k < n; ++k) {
+        const Region& r = all[k];
+        const Region* other = written && written->to > r.from ? written
+                              : r.name && read && read->to > r.from ? read : nullptr;
+        if (other)
+            return fail(MOE_ERR_INVALID_ARG, "%s of tensor %d overlaps %s of tensor %d", r.name ? r.name : "grad",
+                        r.tensor, other->name ? other->name : "grad", other->tensor);
+        const Region*& most = r.name ? written : read;
+        if (!most || r.to > most->to) most = &r;
+    }
+    return MOE_OK;
+}
+
+int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, const moe_adamw_hyper* hyper, int32_t bits,
+              void* stream) {
+    moe::clear_error();
+    if (bits != 8 && bits != 32) return fail(MOE_ERR_INVALID_ARG, "bits = %d: 8 or 32", bits);
+    if (count < 0 || count > (1 << 20)) return fail(MOE_ERR_INVALID_ARG, "count = %d outside [0, 2^20]", count);
+    if (!hyper) return fail(MOE_ERR_INVALID_ARG, "hyper is NULL");
+    if (count > 0 && !tensors) return fail(MOE_ERR_INVALID_ARG, "tensors is NULL");
+    const struct {
+        double v;
+        const char* name;
+        bool read;
+    } rates[5] = {{hyper->lr, "lr", !hyper->lr_device}, {hyper->beta1, "beta1", true}, {hyper->beta2, "beta2", true},
+                  {hyper->eps, "eps", true}, {hyper->weight_decay, "weight_decay", true}};
+    for (int i = 0; i < 5; ++i) {
+        const bool beta = i == 1 || i == 2;
+        if (rates[i].read && !(rates[i].v >= 0 && (beta ? rates[i].v < 1 : std::isfinite(rates[i].v))))
+            return fail(MOE_ERR_INVALID_ARG, "%s = %g outside %s", rates[i].name, rates[i].v,
+                        beta ? "[0, 1)" : "[0, infinity)");
+    }
+    if (!hyper->step_device && hyper->step < 1)
+        return fail(MOE_ERR_INVALID_ARG, "step = %lld: the first is 1", (long long)hyper->step);
+    if (hyper->step_device) CHECK(check_ptr(hyper->step_device, "step_device", 4));
+    if (hyper->lr_device) CHECK(check_ptr(hyper->lr_device, "lr_device", 4));
+    if (hyper->grad_scale) CHECK(check_ptr(hyper->grad_scale, "grad_scale", 4));
+    int64_t all = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        const moe_adamw_tensor& t = tensors[i];
+        if (t.n < 0 || t.n > moe::kAdamwMost || (all += t.n) > moe::kAdamwMost)
+            return fail(MOE_ERR_INVALID_ARG, "n = %lld of tensor %d: together [0, 2^34]", (long long)t.n, i);
+        if (t.n == 0) continue;
+        CHECK(check_ptr(t.param, "param", t.param_fp32 ? 4 : 2));
+        CHECK(check_ptr(t.grad, "grad", t.grad_fp32 ? 4 : 2));
+        if (t.master) CHECK(check_ptr(t.master, "master"));
+        CHECK(check_ptr(t.m, "m"));
+        CHECK(check_ptr(t.v, "v"));
+        if (bits == 8) {
+            CHECK(check_ptr(t.m_scale, "m_scale", 4));
+            CHECK(check_ptr(t.v_scale, "v_scale", 4));
+        } else if (t.m_scale || t.v_scale) {
+            return fail(MOE_ERR_INVALID_ARG, "m_scale and v_scale of tensor %d with bits 32", i);
+        }
+    }
+    if (all == 0) return MOE_OK;
+    CHECK(check_adamw_apart(tensors, count, bits));
+    CHECK(moe::device_ok());
+    HIP_CHECK(moe::launch_adamw(tensors, count, *hyper, bits, static_cast<hipStream_t>(stream)), "adamw launch");
     return MOE_OK;
 }
 
