@@ -406,6 +406,29 @@ int moe_linear_dz(const uint16_t *dy, const uint16_t *z, int32_t act, int64_t T,
                   void *stream);
 
 /*
+ * Gated block: both up-projections, the activation and the product in one pass, with
+ * the gradient back to them. Rows s of group e, as in moe_grouped_matmul (NULL offsets with E = 1: a
+ * dense block):
+ *   moe_gated:     z[s] = [g | u] = x[s] W_e^T + bias,   y[s] = act(g) u
+ *                  x [P, d], w [E, 2h, d]: h gate rows, then the h up rows; bias fp32 [2h] or NULL
+ *                  (dense alone); y [P, h]. z [P, 2h] receives g and u, rounded, for the gradient (NULL:
+ *                  not wanted; y comes from the unrounded sums).
+ *   moe_gated_dz:  dh[s] = dy[s] W2_e,   dz[s] = [dh u act'(g) | dh act(g)]
+ *                  dy [P, d] the gradient of the down-projection's output, w2 [E, d, h], z [P, 2h]; dz
+ *                  [P, 2h], which may be the same buffer as z; y [P, h] receives act(g) u again, from
+ *                  which (with dy) W2's gradient follows (NULL: not wanted). dh is never rounded.
+ * The gradients of x and W are then moe_grouped_matmul_dx / _dw of dz with N = 2h, that of bias
+ * moe_linear_dz of dz (act none). d and h are multiples of 8, h at most 2^19 and, for
+ * moe_gated, (h + 256) d at most 2^31. Rows outside every group are left as they were.
+ */
+int moe_gated(const uint16_t *x, const uint16_t *w, const float *bias, const int32_t *offsets,
+              int32_t act, int64_t P, int64_t E, int64_t h, int64_t d, uint16_t *y, uint16_t *z,
+              void *stream);
+int moe_gated_dz(const uint16_t *dy, const uint16_t *w2, const uint16_t *z, const int32_t *offsets,
+                 int32_t act, int64_t P, int64_t E, int64_t h, int64_t d, uint16_t *dz, uint16_t *y,
+                 void *stream);
+
+/*
  * SwiGLU of rows that hold both up-projections side by side, z = [g | u] [rows, 2h]:
  * y = silu(g) * u [rows, h]; and its gradient dz = [dy u silu'(g) | dy silu(g)]
  * [rows, 2h], which may be the same buffer as z.

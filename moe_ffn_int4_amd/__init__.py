@@ -151,6 +151,10 @@ def lib() -> ctypes.CDLL:
         L.moe_linear_dz_workspace_bytes.restype = sz
         L.moe_linear_dz.argtypes = [P, P, i32, i64, i64, P, P, P, sz, P]
         L.moe_linear_dz.restype = ctypes.c_int
+        L.moe_gated.argtypes = [P, P, P, P, i32, i64, i64, i64, i64, P, P, P]
+        L.moe_gated.restype = ctypes.c_int
+        L.moe_gated_dz.argtypes = [P, P, P, P, i32, i64, i64, i64, i64, P, P, P]
+        L.moe_gated_dz.restype = ctypes.c_int
         L.moe_swiglu.argtypes = [P, i64, i64, P, P]
         L.moe_swiglu.restype = ctypes.c_int
         L.moe_swiglu_backward.argtypes = [P, P, i64, i64, P, P]
@@ -829,6 +833,81 @@ def linear_dw(dz: torch.Tensor, x: torch.Tensor, out: Optional[torch.Tensor] = N
     _run(lib().moe_grouped_matmul_dw, dz, dz.data_ptr(), x.data_ptr(), None, T, 1, N, K,
          dw.data_ptr(), dw.dtype == torch.float32, bool(accumulate))
     return dw
+
+
+def _gated(x, w, bias, offsets, act, z, out, E, h2, d):
+    P = x.shape[0]
+    if x.shape[1] != d:
+        raise ValueError(f"x has {x.shape[1]} columns, w {d}")
+    if h2 % 2:
+        raise ValueError("w must have as many gate rows as up rows")
+    h = h2 // 2
+    if z is not None:
+        _need(z, "z", torch.bfloat16, (P, h2))
+    _same_device(x, w, bias, offsets, z)
+    y = _output(out, "out", (P, h), torch.bfloat16, x)
+    _run(lib().moe_gated, x, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(offsets), _act(act), P, E, h, d,
+         y.data_ptr(), _ptr(z))
+    return y
+
+
+def grouped_gated(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, act: str = "silu",
+                  z: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Both up-projections of each expert's rows, the activation and the product in one pass: y[s] =
+    act(g) * u with [g | u] = x[s] w[e]^T.
+
+    x bf16 [P, d] (rows in expert order), w bf16 [E, 2h, d], the gate's h rows first, offsets int32
+    [E+1] (``route``), act one of ``ACTS``, y bf16 [P, h]. ``z`` (bf16 [P, 2h]), if given, receives [g | u]
+    for ``grouped_gated_dz``. What ``grouped_matmul`` and ``swiglu`` do in two passes, with z."""
+    _two_dim(x, "x")
+    E, h2, d = _groups(w, offsets, x)
+    return _gated(x, w, None, offsets, act, z, out, E, h2, d)
+
+
+def gated_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "silu",
+                 z: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``grouped_gated`` of one dense block: w bf16 [2h, d], bias fp32 [2h] (its gradient: ``linear_dz`` of dz
+    with act "none")."""
+    _two_dim(x, "x")
+    _two_dim(w, "w")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (w.shape[0],))
+    return _gated(x, w, bias, None, act, z, out, 1, w.shape[0], w.shape[1])
+
+
+def _gated_dz(dy, w2, z, offsets, act, y, out, E, d, h):
+    P = dy.shape[0]
+    if dy.shape[1] != d:
+        raise ValueError(f"dy has {dy.shape[1]} columns, w2 {d} rows")
+    _need(z, "z", torch.bfloat16, (P, 2 * h))
+    if y is not None:
+        _need(y, "y", torch.bfloat16, (P, h))
+    _same_device(dy, w2, z, offsets, y)
+    dz = _output(out, "out", (P, 2 * h), torch.bfloat16, dy)
+    _run(lib().moe_gated_dz, dy, dy.data_ptr(), w2.data_ptr(), z.data_ptr(), _ptr(offsets), _act(act), P, E, h, d,
+         dz.data_ptr(), _ptr(y))
+    return dz
+
+
+def grouped_gated_dz(dy: torch.Tensor, w2: torch.Tensor, z: torch.Tensor, offsets: torch.Tensor, act: str = "silu",
+                     y: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of a gated block's projections, from that of the down-projection's output: dz[s] =
+    [dh u act'(g) | dh act(g)], bf16 [P, 2h], with dh = dy[s] w2[e].
+
+    dy bf16 [P, d], w2 bf16 [E, d, h] (the weights of ``grouped_matmul`` behind the block), z = [g | u] bf16
+    [P, 2h]. ``y`` (bf16 [P, h]), if given, receives act(g) * u, of which w2's gradient is made, so that the
+    forward need not keep it. ``out`` may be z. Then ``grouped_matmul_dx`` and ``_dw`` of dz."""
+    _two_dim(dy, "dy")
+    E, d, h = _groups(w2, offsets, dy)
+    return _gated_dz(dy, w2, z, offsets, act, y, out, E, d, h)
+
+
+def gated_linear_dz(dy: torch.Tensor, w2: torch.Tensor, z: torch.Tensor, act: str = "silu",
+                    y: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``grouped_gated_dz`` of one dense block: w2 bf16 [d, h]."""
+    _two_dim(dy, "dy")
+    _two_dim(w2, "w2")
+    return _gated_dz(dy, w2, z, None, act, y, out, 1, w2.shape[0], w2.shape[1])
 
 
 def swiglu(z: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:

@@ -17,6 +17,8 @@
 // 8-byte reads of gfx950 (16 lanes read 4 rows of 16 values and each gets a column).
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "train.h"
 
@@ -246,6 +248,14 @@ __device__ __forceinline__ int red_spread(int r) {
     return (((r >> 3) & 1) << 3) | ((r & 3) << 1);
 }
 
+// Tile row i of a gated block's weights: 16 gate rows, then the 16 up rows of the same
+// outputs, and so on, so that a wave's neighbouring sub-tiles are the two factors of a
+// product and meet in one lane's registers. `valid`: rows of both in the tile.
+__device__ __forceinline__ int64_t gated_row(int i, int valid, int64_t apart) {
+    const int out = (i >> 5) * 16 + (i & 15), last = (valid >> 1) - 1;
+    return (out < last ? out : last) + ((i >> 4) & 1) * apart;
+}
+
 // Global -> LDS staging of one operand's tile, 1 KB a wave and load.
 // TR: m / n contiguous.
 template <bool TR, int SIZE, int WAVES>
@@ -261,7 +271,10 @@ struct Stager {
     // TR = false: tile row i is row i of `p` (ld values apart), rows past `valid`
     // repeat the last one. TR = true: tile row i is row i of the reduction, values
     // past `valid` (a multiple of 8) repeat the last piece. What they give is dropped.
-    __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int valid, int wave_, int lane_) {
+    // GATED: tile rows are those of two matrices `apart` rows apart, by turns (gated_row).
+    template <bool GATED = false>
+    __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int valid, int wave_, int lane_,
+                                         int64_t apart = 0) {
         wave = wave_;
         lane = lane_;
         base = reinterpret_cast<const uint8_t*>(uniform(reinterpret_cast<uint64_t>(p)));
@@ -274,7 +287,8 @@ struct Stager {
                 c = c < valid ? c : valid - 8;
                 off[i] = static_cast<uint32_t>((r * ld + c) * 2);
             } else {
-                off[i] = static_cast<uint32_t>(((r < valid ? r : valid - 1) * ld + piece(i) * 8) * 2);
+                const int64_t m = GATED ? gated_row(r, valid, apart) : r < valid ? r : valid - 1;
+                off[i] = static_cast<uint32_t>((m * ld + piece(i) * 8) * 2);
             }
         }
     }
@@ -584,10 +598,146 @@ __device__ __forceinline__ void store_applied(const MatmulArgs& a, const f32x4 (
     }
 }
 
+// N values to bf16, N 8 or 4
+template <int N>
+__device__ __forceinline__ void store_bf16(uint16_t* p, const float* v) {
+    typedef uint32_t words __attribute__((ext_vector_type(N / 2)));
+    words w;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16x2_rn(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<words*>(p) = w;
+}
+
+// A gated block's outputs from sub-tiles that are gate and up by turns: each two give 16
+// columns of act(g) u. A pair of them (JJ = 2) goes out eight columns a lane, as above, a
+// single one four. z takes g and u as they were before the activation, rounded.
+template <int ACT, int NI, int JJ, typename Row>
+__device__ __forceinline__ void store_gated(const MatmulArgs& a, const f32x4 (*acc)[2 * JJ], const Place& at,
+                                            Row&& row0, int lane) {
+    constexpr int W = 4 * JJ;  // columns a lane
+    const int i16 = lane & 15, q = lane >> 4;
+    const int64_t h = a.N / 2;
+    const int c = at.col0 / 2 + (JJ == 2 ? eight_columns_at(q) : 4 * q);
+    const int64_t col = at.out_col / 2 + c;
+    const bool inside = c < at.cols / 2;
+    float bg[W], bu[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) bg[k] = bu[k] = 0.f;
+    if (a.bias && inside) {
+#pragma unroll
+        for (int k = 0; k < W; k += 4) {
+            *reinterpret_cast<f32x4*>(bg + k) = *reinterpret_cast<const f32x4*>(a.bias + col + k);
+            *reinterpret_cast<f32x4*>(bu + k) = *reinterpret_cast<const f32x4*>(a.bias + h + col + k);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        float g[W], u[W];
+        if constexpr (JJ == 2) {
+            eight_columns(acc[i][0], acc[i][2], g);
+            eight_columns(acc[i][1], acc[i][3], u);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                g[k] = acc[i][0][k];
+                u[k] = acc[i][1][k];
+            }
+        }
+        const int r0 = row0(i), r = r0 + i16;
+        if (r0 < 0 || r >= at.rows || !inside) continue;
+        const int64_t row = at.out_row + r;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            g[k] += bg[k];
+            u[k] += bu[k];
+        }
+        if (a.z) {
+            store_bf16<W>(a.z + row * a.N + col, g);
+            store_bf16<W>(a.z + row * a.N + h + col, u);
+        }
+#pragma unroll
+        for (int k = 0; k < W; ++k) g[k] = act_value(g[k], ACT) * u[k];
+        store_bf16<W>(static_cast<uint16_t*>(a.out) + row * h + col, g);
+    }
+}
+
+// The gradient of a gated block's projections, from that of its outputs (the products):
+// dz = [dh u act'(g) | dh act(g)], and act(g) u where it is wanted. g and u are loaded for two
+// sub-tile rows at once, ahead of the stores. Each place of dz is written by the lane
+// that read it of z, so that they may be one buffer.
+template <int ACT, int NI, int JJ, typename Row>
+__device__ __forceinline__ void store_gated_dz(const MatmulArgs& a, const f32x4 (*acc)[2 * JJ], const Place& at,
+                                               Row&& row0, int lane) {
+    constexpr int BATCH = 2;
+    const int i16 = lane & 15, q = lane >> 4;
+    const int64_t h = a.K;
+    uint16_t* dz = static_cast<uint16_t*>(a.out);
+#pragma unroll
+    for (int i0 = 0; i0 < NI; i0 += BATCH) {
+        u32x4 z[BATCH][JJ][2];
+        bool ok[BATCH][JJ];
+        int64_t row[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int r0 = row0(i0 + b), r = r0 + i16;
+            row[b] = at.out_row + r;
+#pragma unroll
+            for (int j = 0; j < JJ; ++j) {
+                const int c = at.col0 + 32 * j + eight_columns_at(q);
+                ok[b][j] = r0 >= 0 && r < at.rows && c < at.cols;
+                if (!ok[b][j]) continue;
+                const uint16_t* p = a.gate_z + row[b] * 2 * h + at.out_col + c;
+                z[b][j][0] = *reinterpret_cast<const u32x4*>(p);
+                z[b][j][1] = *reinterpret_cast<const u32x4*>(p + h);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+            for (int j = 0; j < JJ; ++j) {
+                float d[8], g[8], u[8];
+                eight_columns(acc[i0 + b][2 * j], acc[i0 + b][2 * j + 1], d);
+                if (!ok[b][j]) continue;
+                unpack8(z[b][j][0], g);
+                unpack8(z[b][j][1], u);
+                const int64_t col = at.out_col + at.col0 + 32 * j + eight_columns_at(q);
+                float dg[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float v = act_value(g[k], ACT);
+                    dg[k] = d[k] * u[k] * act_slope(g[k], ACT);
+                    d[k] *= v;
+                    u[k] *= v;
+                }
+                store_bf16<8>(dz + row[b] * 2 * h + col, dg);
+                store_bf16<8>(dz + row[b] * 2 * h + h + col, d);
+                if (a.gate_y) store_bf16<8>(a.gate_y + row[b] * h + col, u);
+            }
+    }
+}
+
+template <Epilogue EPI, int ACT, int NI, int JJ, typename Row>
+__device__ __forceinline__ void store_gated_any(const MatmulArgs& a, const f32x4 (*acc)[2 * JJ], const Place& at,
+                                                Row&& row0, int lane) {
+    if constexpr (EPI == Epilogue::kGated) store_gated<ACT, NI, JJ>(a, acc, at, row0, lane);
+    else store_gated_dz<ACT, NI, JJ>(a, acc, at, row0, lane);
+}
+
 // All of a wave's results.
-template <int MODE, bool LINEAR, int NI, int JJ, typename Row>
+template <int MODE, Epilogue EPI, int NI, int JJ, typename Row>
 __device__ __forceinline__ void store_all(const MatmulArgs& a, const f32x4 (*acc)[2 * JJ], const Place& at,
                                           Row&& row0, int lane) {
+    if constexpr (EPI == Epilogue::kGated || EPI == Epilogue::kGatedDz) {
+        // the activation as a compile-time constant, as below
+        switch (a.act) {
+            case MOE_ACT_RELU: return store_gated_any<EPI, MOE_ACT_RELU, NI, JJ>(a, acc, at, row0, lane);
+            case MOE_ACT_SILU: return store_gated_any<EPI, MOE_ACT_SILU, NI, JJ>(a, acc, at, row0, lane);
+            case MOE_ACT_GELU: return store_gated_any<EPI, MOE_ACT_GELU, NI, JJ>(a, acc, at, row0, lane);
+            case MOE_ACT_GELU_TANH: return store_gated_any<EPI, MOE_ACT_GELU_TANH, NI, JJ>(a, acc, at, row0, lane);
+            default: return store_gated_any<EPI, MOE_ACT_NONE, NI, JJ>(a, acc, at, row0, lane);
+        }
+    }
+    constexpr bool LINEAR = EPI == Epilogue::kLinear;
     if (LINEAR && (a.bias || a.z || a.residual || a.act != MOE_ACT_NONE)) {
         switch (a.act) {
             case MOE_ACT_RELU: return store_applied<true, MOE_ACT_RELU, NI, JJ>(a, acc, at, row0, lane);
@@ -620,6 +770,36 @@ __device__ __forceinline__ void store1(const MatmulArgs& a, int64_t row, int64_t
     else static_cast<uint16_t*>(a.out)[at] = static_cast<uint16_t>(pack_bf16x2_rn(v, 0.f));
 }
 
+// One output of a gated block from its two factors.
+__device__ __forceinline__ void store1_gated(const MatmulArgs& a, int64_t row, int64_t col, float g, float u) {
+    const int64_t h = a.N / 2;
+    if (a.bias) {
+        g += a.bias[col];
+        u += a.bias[h + col];
+    }
+    if (a.z) {
+        a.z[row * a.N + col] = static_cast<uint16_t>(pack_bf16x2_rn(g, 0.f));
+        a.z[row * a.N + h + col] = static_cast<uint16_t>(pack_bf16x2_rn(u, 0.f));
+    }
+    static_cast<uint16_t*>(a.out)[row * h + col] =
+        static_cast<uint16_t>(pack_bf16x2_rn(act_value(g, a.act) * u, 0.f));
+}
+
+// calls `f` with a launch's direction and epilogue as compile-time constants
+template <typename F>
+inline hipError_t with_mode(int mode, Epilogue e, F&& f) {
+    using std::integral_constant;
+    if (mode == kDw) return f(integral_constant<int, kDw>{}, integral_constant<Epilogue, Epilogue::kPlain>{});
+    if (mode == kDx) {
+        if (e == Epilogue::kGatedDz)
+            return f(integral_constant<int, kDx>{}, integral_constant<Epilogue, Epilogue::kGatedDz>{});
+        return f(integral_constant<int, kDx>{}, integral_constant<Epilogue, Epilogue::kPlain>{});
+    }
+    if (e == Epilogue::kGated) return f(integral_constant<int, kFwd>{}, integral_constant<Epilogue, Epilogue::kGated>{});
+    if (e == Epilogue::kLinear) return f(integral_constant<int, kFwd>{}, integral_constant<Epilogue, Epilogue::kLinear>{});
+    return f(integral_constant<int, kFwd>{}, integral_constant<Epilogue, Epilogue::kPlain>{});
+}
+
 // The operands of one tile as C[m][n] = sum_r A(m, r) B(n, r).
 template <int MODE>
 struct Operands {
@@ -631,8 +811,9 @@ struct Operands {
 };
 
 // part: 0 or 1 for the first or last BM / 2 rows of the tile, -1 for all; `rows` is not
-// positive for a half that has none
-template <int MODE, int BM, int BN>
+// positive for a half that has none. A gated block's columns are rows of both its matrices, b
+// at the first of its gate rows.
+template <int MODE, int BM, int BN, Epilogue EPI>
 __device__ __forceinline__ Operands<MODE> operands(const MatmulArgs& a, const MatTile& t, int rt, int ct,
                                                    int part) {
     const int skip = part > 0 ? BM / 2 : 0, most = part < 0 ? BM : BM / 2;
@@ -656,7 +837,7 @@ __device__ __forceinline__ Operands<MODE> operands(const MatmulArgs& a, const Ma
         const uint16_t* w = a.b + static_cast<int64_t>(t.group) * a.N * a.K;
         const int64_t row0 = t.row0 + skip;
         o.a = a.a + row0 * kd;
-        o.b = MODE == kFwd ? w + o.col0 * a.K : w + o.col0;
+        o.b = MODE == kFwd ? w + (EPI == Epilogue::kGated ? o.col0 / 2 : o.col0) * a.K : w + o.col0;
         o.lda = kd;
         o.ldb = a.K;
         o.red = kd;

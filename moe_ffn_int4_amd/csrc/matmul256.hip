@@ -236,16 +236,19 @@ struct HalfStager {
         const int r = row(i, wave, lane);
         return TR ? (lane & 15) ^ red_spread<128>(r) : (lane & 7) ^ row_spread(r);
     }
+    // GATED: rows of two matrices `apart` rows apart, by turns (gated_row)
+    template <bool GATED = false>
     __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int valid, int each0, int each1,
-                                         int wave, int lane) {
+                                         int wave, int lane, int64_t apart = 0) {
         base = reinterpret_cast<const uint8_t*>(uniform(reinterpret_cast<uint64_t>(p)));
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = row(i, wave, lane), c = piece(i, wave, lane) * 8;
-                int m = half_index<B>(TR ? c : r, h, h ? each1 : each0);
-                m = m < valid ? m : valid - (TR ? 8 : 1);
+                int64_t m = half_index<B>(TR ? c : r, h, h ? each1 : each0);
+                if (GATED) m = gated_row(static_cast<int>(m), valid, apart);
+                else m = m < valid ? m : valid - (TR ? 8 : 1);
                 off[h][i] = static_cast<uint32_t>((TR ? r * ld + m : m * ld + c) * 2);
             }
     }
@@ -291,7 +294,20 @@ struct Work {
         sb.load(p + B0, 0, k, static_cast<int>(a.K), red, wave, lane);
         sb.load(p + B1, 1, k, static_cast<int>(a.K), red, wave, lane);
     }
+    // The uniform values in scalar registers again: through the branches of a gated block's stores
+    // the compiler carries them from tile to tile in vector registers.
+    __device__ __forceinline__ void settle() {
+        sa.base = reinterpret_cast<const uint8_t*>(uniform(reinterpret_cast<uint64_t>(sa.base)));
+        sb.base = reinterpret_cast<const uint8_t*>(uniform(reinterpret_cast<uint64_t>(sb.base)));
+        red = __builtin_amdgcn_readfirstlane(red);
+        steps = __builtin_amdgcn_readfirstlane(steps);
+        rows = __builtin_amdgcn_readfirstlane(rows);
+        cols = __builtin_amdgcn_readfirstlane(cols);
+        col0 = __builtin_amdgcn_readfirstlane(col0);
+        out_row = uniform(out_row);
+    }
     // steps 0 and 1 but for step 1's A1: 6 + 2 + 6 loads a wave (small tiles: 6 + 6)
+    template <Epilogue EPI>
     __device__ __forceinline__ void start(const MatmulArgs& a, const Operands<MODE>& o, uint32_t at, int wave,
                                           int lane) {
         red = __builtin_amdgcn_readfirstlane(static_cast<int>(o.red));
@@ -303,7 +319,7 @@ struct Work {
         steps = (red + kStepR - 1) / kStepR;
         if (steps == 0) return;
         sa.init(o.a, o.lda, rows, small ? rows_each(rows) : 64, small ? 0 : rows_each(rows - 128), wave, lane);
-        sb.init(o.b, o.ldb, cols, 0, 0, wave, lane);
+        sb.template init<EPI == Epilogue::kGated>(o.b, o.ldb, cols, 0, 0, wave, lane, a.N / 2);
         request(a, at, 0, wave, lane);
         if (!small) load_a(a, at + A1, 1, 0, wave, lane);
         if (steps > 1) request(a, at + (small ? 3 * kHalf : 4 * kHalf), 1, wave, lane);
@@ -314,9 +330,10 @@ struct Work {
 
 // The products of a tile that `start` has been called for; then `next()`, which may
 // request the next tile's first steps, then the stores.
-template <int MODE, bool LINEAR, bool SMALL, typename Next>
-__device__ __forceinline__ void run_tile(const MatmulArgs& a, const Work<MODE>& w, uint8_t* lds, int wave,
+template <int MODE, Epilogue EPI, bool SMALL, typename Next>
+__device__ __forceinline__ void run_tile(const MatmulArgs& a, Work<MODE>& w, uint8_t* lds, int wave,
                                          int lane, Next&& next) {
+    if constexpr (EPI == Epilogue::kGated || EPI == Epilogue::kGatedDz) w.settle();
     const int wm = wave >> 2, wn = wave & 3;
     Reader<Work<MODE>::AT, 128> ra;
     Reader<Work<MODE>::BT, 128> rb;
@@ -425,7 +442,7 @@ __device__ __forceinline__ void run_tile(const MatmulArgs& a, const Work<MODE>& 
 
     // opaque, so that the addresses are not computed once for all tiles and kept
     asm volatile("" : "+v"(lane));
-    store_all<MODE, LINEAR, MI, 2>(
+    store_all<MODE, EPI, MI, 2>(
         a, acc, Place{out_row, ldo, col0, rows, wn * 64, cols},
         [&](int i) {
             if ((SMALL || i >= 4) && (i & 3) > 0 && (i & 3) >= subs) return -1000000;
@@ -436,7 +453,7 @@ __device__ __forceinline__ void run_tile(const MatmulArgs& a, const Work<MODE>& 
 
 // Blocks walk their XCD's tiles in a round robin; a block requests its next tile's
 // first two steps before it stores a tile.
-template <int MODE, bool LINEAR>
+template <int MODE, Epilogue EPI>
 __global__ __launch_bounds__(64 * kWaves, 2) void matmul256_kernel(MatmulArgs a) {
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int lane = threadIdx.x & 63;
@@ -467,7 +484,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul256_kernel(MatmulArgs a)
     auto start = [&]() __attribute__((always_inline)) {
         int lane_ = lane;
         asm volatile("" : "+v"(lane_));
-        if (more) w.start(a, operands<MODE, BM, BN>(a, t, rt, ct, part), at, wave, lane_);
+        if (more) w.template start<EPI>(a, operands<MODE, BM, BN, EPI>(a, t, rt, ct, part), at, wave, lane_);
     };
     find_next();
     if (!more) return;
@@ -476,8 +493,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul256_kernel(MatmulArgs a)
         const bool small = w.small;
         find_next();
         going = more;
-        if (small) run_tile<MODE, LINEAR, true>(a, w, lds, wave, lane, start);
-        else run_tile<MODE, LINEAR, false>(a, w, lds, wave, lane, start);
+        if (small) run_tile<MODE, EPI, true>(a, w, lds, wave, lane, start);
+        else run_tile<MODE, EPI, false>(a, w, lds, wave, lane, start);
     }
 }
 
@@ -494,10 +511,10 @@ static int64_t matmul256_blocks(const MatmulArgs& a) {
     return 8 * ((a.P / BM + groups) * ncol / 8 + 2 * groups + 1 + kXcdCus / 2);
 }
 
-template <int MODE, bool LINEAR>
+template <int MODE, Epilogue EPI>
 static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     static LdsDevices allowed;
-    const hipError_t e = allow_lds(reinterpret_cast<const void*>(&matmul256_kernel<MODE, LINEAR>),
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(&matmul256_kernel<MODE, EPI>),
                                    kStages + kTable, allowed);
     if (e != hipSuccess) return e;
     // Persistent blocks, one a CU, where the tiles cost about the same (a dense
@@ -508,15 +525,14 @@ static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     int64_t blocks = matmul256_blocks<MODE>(a);
     if ((MODE == kDw || a.E == 1) && blocks > 256) blocks = 256;
     if (blocks > kGridX) blocks = kGridX;  // of several tiles each
-    hipLaunchKernelGGL((matmul256_kernel<MODE, LINEAR>), dim3(static_cast<unsigned>(blocks)),
+    hipLaunchKernelGGL((matmul256_kernel<MODE, EPI>), dim3(static_cast<unsigned>(blocks)),
                        dim3(64 * kWaves), kStages + kTable, stream, a);
     return hipGetLastError();
 }
 
-hipError_t launch_matmul256(int mode, bool linear, const MatmulArgs& a, hipStream_t stream) {
-    if (mode == kDx) return launch<kDx, false>(a, stream);
-    if (mode == kDw) return launch<kDw, false>(a, stream);
-    return linear ? launch<kFwd, true>(a, stream) : launch<kFwd, false>(a, stream);
+hipError_t launch_matmul256(int mode, Epilogue epilogue, const MatmulArgs& a, hipStream_t stream) {
+    return with_mode(mode, epilogue,
+                     [&](auto m, auto e) { return launch<decltype(m)::value, decltype(e)::value>(a, stream); });
 }
 
 }  // namespace moe

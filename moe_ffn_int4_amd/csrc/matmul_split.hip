@@ -22,7 +22,7 @@ constexpr int kLds = kWaves * kRing * kStage;
 constexpr int kBand = 8;
 }  // namespace
 
-template <int MODE, bool LINEAR>
+template <int MODE, Epilogue EPI>
 __global__ __launch_bounds__(64 * kWaves, 2) void matmul_split_kernel(MatmulArgs a) {
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int lane = threadIdx.x & 63;
@@ -30,13 +30,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_split_kernel(MatmulArgs
     MatTile t;
     int rt, ct;
     if (!find_tile<MODE, T, T, kBand>(a, lane, t, rt, ct)) return;
-    const Operands<MODE> o = operands<MODE, T, T>(a, t, rt, ct, -1);
+    const Operands<MODE> o = operands<MODE, T, T, EPI>(a, t, rt, ct, -1);
 
     constexpr bool AT = MODE == kDw, BT = MODE != kFwd;
     Stager<AT, T, 1> sa;
     Stager<BT, T, 1> sb;
     sa.init(o.a, o.lda, o.rows, 0, lane);
-    sb.init(o.b, o.ldb, o.cols, 0, lane);
+    sb.template init<EPI == Epilogue::kGated>(o.b, o.ldb, o.cols, 0, lane, a.N / 2);
     Reader<AT, T> ra;
     Reader<BT, T> rb;
     ra.init(0, lane);
@@ -95,24 +95,23 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_split_kernel(MatmulArgs
     for (int w = 1; w < kWaves; ++w)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] += sums[w * kEach + i * 64];
-    store_all<MODE, LINEAR, 2, 1>(a, acc, Place{o.out_row, o.ldo, o.col0, o.rows, 0, o.cols},
+    store_all<MODE, EPI, 2, 1>(a, acc, Place{o.out_row, o.ldo, o.col0, o.rows, 0, o.cols},
                                   [&](int i) { return 16 * i; }, lane);
 }
 
-template <int MODE, bool LINEAR>
+template <int MODE, Epilogue EPI>
 static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     static LdsDevices allowed;
-    const hipError_t e = allow_lds(reinterpret_cast<const void*>(&matmul_split_kernel<MODE, LINEAR>), kLds, allowed);
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(&matmul_split_kernel<MODE, EPI>), kLds, allowed);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((matmul_split_kernel<MODE, LINEAR>), block_grid(matmul_blocks<MODE, T, T>(a)),
+    hipLaunchKernelGGL((matmul_split_kernel<MODE, EPI>), block_grid(matmul_blocks<MODE, T, T>(a)),
                        dim3(64 * kWaves), kLds, stream, a);
     return hipGetLastError();
 }
 
-hipError_t launch_matmul_split(int mode, bool linear, const MatmulArgs& a, hipStream_t stream) {
-    if (mode == kDx) return launch<kDx, false>(a, stream);
-    if (mode == kDw) return launch<kDw, false>(a, stream);
-    return linear ? launch<kFwd, true>(a, stream) : launch<kFwd, false>(a, stream);
+hipError_t launch_matmul_split(int mode, Epilogue epilogue, const MatmulArgs& a, hipStream_t stream) {
+    return with_mode(mode, epilogue,
+                     [&](auto m, auto e) { return launch<decltype(m)::value, decltype(e)::value>(a, stream); });
 }
 
 }  // namespace moe

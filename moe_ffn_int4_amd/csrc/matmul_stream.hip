@@ -60,16 +60,19 @@ __device__ __forceinline__ int seg_spread(int row) { return row & 15; }
 
 // The strips of a launch, 16 weight rows of one row tile each, are dealt to the blocks in
 // turn. A wave's chunks of all its strips are one sequence, whose ring goes on from strip to strip.
-template <typename S, bool LINEAR>
+template <typename S, Epilogue EPI>
 __global__ __launch_bounds__(64 * kWaves, 2) void matmul_stream_kernel(MatmulArgs a, int rings) {
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr bool GATED = EPI == Epilogue::kGated;
+    // one group of all rows: linear's, and a gated block's without offsets
+    const bool dense = EPI == Epilogue::kLinear || (GATED && !a.offsets);
     RowTiles<S::MX> tiles;
-    if (LINEAR) tiles.total = static_cast<int>((a.P + S::MX - 1) / S::MX);
+    if (dense) tiles.total = static_cast<int>((a.P + S::MX - 1) / S::MX);
     else tiles.scan(a, lane);
     auto find = [&](int rt) __attribute__((always_inline)) {
-        return LINEAR ? dense_tile<S::MX>(a, rt) : tiles.find(rt, lane);
+        return dense ? dense_tile<S::MX>(a, rt) : tiles.find(rt, lane);
     };
     const int strips = static_cast<int>((a.N + kRowsN - 1) / kRowsN);
     const int stride = static_cast<int>(gridDim.x);
@@ -95,7 +98,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_stream_kernel(MatmulArg
     uint32_t off[S::kLoads];
     int asked = first, ask = 0, ask_at = 0;
     auto open_strip = [&]() __attribute__((always_inline)) {
-        const int rt = asked / strips, n0 = (asked - rt * strips) * kRowsN;
+        const int rt = asked / strips, n0 = (asked - rt * strips) * (GATED ? kRowsN / 2 : kRowsN);
         const MatTile t = find(rt);
         const int nw = static_cast<int>(a.N - n0 < kRowsN ? a.N - n0 : kRowsN);
         w = reinterpret_cast<const uint8_t*>(
@@ -106,7 +109,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_stream_kernel(MatmulArg
             const bool isw = i < S::kLoadsW;
             const int r = (isw ? i : i - S::kLoadsW) * S::kPerLoad + lrow;
             const int most = isw ? nw : t.nrows;
-            off[i] = static_cast<uint32_t>((r < most ? r : most - 1) * K * 2 + ((slot ^ seg_spread(r)) * 16));
+            // a gated block's strip: eight gate rows and the up rows of the same outputs
+            const int64_t row = GATED && isw ? (r & 7) + (r >> 3) * (a.N / 2) : r < most ? r : most - 1;
+            off[i] = static_cast<uint32_t>(row * K * 2 + ((slot ^ seg_spread(r)) * 16));
         }
     };
     // the next chunk of this block's strips, if any
@@ -178,27 +183,36 @@ __global__ __launch_bounds__(64 * kWaves, 2) void matmul_stream_kernel(MatmulArg
         };
         *reinterpret_cast<f32x4*>(sums_of(wave) + i16 * kRowsN + 4 * q) = acc[0] + acc[1];
         block_barrier_lds();
-        const int rt = strip / strips, n0 = (strip - rt * strips) * kRowsN;
+        const int rt = strip / strips, n0 = (strip - rt * strips) * (GATED ? kRowsN / 2 : kRowsN);
         const MatTile t = find(rt);
         const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
-        float v = sums_of(0)[m * kRowsN + n];
+        float v = sums_of(0)[m * kRowsN + n], up = 0.f;
 #pragma unroll
         for (int i = 1; i < kWaves; ++i) v += sums_of(i)[m * kRowsN + n];
+        if constexpr (GATED) {
+            up = sums_of(0)[m * kRowsN + (n | 8)];
+#pragma unroll
+            for (int i = 1; i < kWaves; ++i) up += sums_of(i)[m * kRowsN + (n | 8)];
+        }
         block_barrier_lds();
-        if (m < t.nrows && n0 + n < a.N) store1<LINEAR>(a, t.row0 + m, a.N, n0 + n, v);
+        if constexpr (GATED) {
+            if (m < t.nrows && n < 8) store1_gated(a, t.row0 + m, n0 + n, v, up);
+        } else {
+            if (m < t.nrows && n0 + n < a.N) store1<EPI == Epilogue::kLinear>(a, t.row0 + m, a.N, n0 + n, v);
+        }
     }
 }
 
-template <typename S, bool LINEAR>
+template <typename S, Epilogue EPI>
 static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     static LdsDevices allowed;
-    const hipError_t e = allow_lds(reinterpret_cast<const void*>(&matmul_stream_kernel<S, LINEAR>), S::kLds, allowed);
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(&matmul_stream_kernel<S, EPI>), S::kLds, allowed);
     if (e != hipSuccess) return e;
     const int64_t partial = a.E < a.P ? a.E : a.P;
     const int64_t strips = (a.P / S::MX + partial) * ((a.N + kRowsN - 1) / kRowsN);
     const int blocks = static_cast<int>(strips < kMostBlocks ? strips : kMostBlocks);
     const int rings = strips > kMostBlocks ? S::RING : ring_chunks<S>(a.K);
-    hipLaunchKernelGGL((matmul_stream_kernel<S, LINEAR>), dim3(blocks), dim3(64 * kWaves),
+    hipLaunchKernelGGL((matmul_stream_kernel<S, EPI>), dim3(blocks), dim3(64 * kWaves),
                        S::kChunk * rings * kWaves, stream, a, rings);
     return hipGetLastError();
 }
@@ -206,11 +220,17 @@ static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
 // The shape goes by the mean group, the sizes being unknown here. A group of more rows than MX
 // streams its weights once for each MX of them: 512 rows over E = 128, 16384 x 5120, take 3.5 ms in
 // groups of four, 2.9 with all rows in one group (tiles of 128 then: 0.11).
-hipError_t launch_matmul_stream(bool linear, const MatmulArgs& a, hipStream_t stream) {
+hipError_t launch_matmul_stream(Epilogue epilogue, const MatmulArgs& a, hipStream_t stream) {
     using Few = StreamShape<4, 256, 2>;
     using Many = StreamShape<16, 128, 2>;
-    if (a.P <= 4 * a.E) return linear ? launch<Few, true>(a, stream) : launch<Few, false>(a, stream);
-    return linear ? launch<Many, true>(a, stream) : launch<Many, false>(a, stream);
+    const bool few = a.P <= 4 * a.E;
+    switch (epilogue) {
+        case Epilogue::kLinear:
+            return few ? launch<Few, Epilogue::kLinear>(a, stream) : launch<Many, Epilogue::kLinear>(a, stream);
+        case Epilogue::kGated:
+            return few ? launch<Few, Epilogue::kGated>(a, stream) : launch<Many, Epilogue::kGated>(a, stream);
+        default: return few ? launch<Few, Epilogue::kPlain>(a, stream) : launch<Many, Epilogue::kPlain>(a, stream);
+    }
 }
 
 }  // namespace moe

@@ -32,7 +32,7 @@ __device__ __forceinline__ void wait_steps(int steps) {
 }
 }  // namespace
 
-template <int MODE, bool LINEAR, int T, int RING, int KS>
+template <int MODE, Epilogue EPI, int T, int RING, int KS>
 __global__ __launch_bounds__(64 * kWaves * KS, KS == 1 ? 2 : KS) void matmul_tile_kernel(MatmulArgs a) {
     constexpr int kTile = T * kStepR * 2;  // one operand of one step
     constexpr int kStage = 2 * kTile;
@@ -44,13 +44,13 @@ __global__ __launch_bounds__(64 * kWaves * KS, KS == 1 ? 2 : KS) void matmul_til
     MatTile t;
     int rt, ct;
     if (!find_tile<MODE, T, T, kBand>(a, lane, t, rt, ct)) return;
-    const Operands<MODE> o = operands<MODE, T, T>(a, t, rt, ct, -1);
+    const Operands<MODE> o = operands<MODE, T, T, EPI>(a, t, rt, ct, -1);
 
     constexpr bool AT = MODE == kDw, BT = MODE != kFwd;
     Stager<AT, T, kWaves> sa;
     Stager<BT, T, kWaves> sb;
     sa.init(o.a, o.lda, o.rows, wave, lane);
-    sb.init(o.b, o.ldb, o.cols, wave, lane);
+    sb.template init<EPI == Epilogue::kGated>(o.b, o.ldb, o.cols, wave, lane, a.N / 2);
     const int wm = (wave >> 1) * (T / 2), wn = (wave & 1) * (T / 2);
     Reader<AT, T> ra;
     Reader<BT, T> rb;
@@ -124,39 +124,39 @@ __global__ __launch_bounds__(64 * kWaves * KS, KS == 1 ? 2 : KS) void matmul_til
             for (int i = 0; i < S * S; ++i) acc[i / S][i % S] += sums[((p - 1) * S * S + i) * 64 * kWaves];
     }
 
-    store_all<MODE, LINEAR, S, S / 2>(a, acc, Place{o.out_row, o.ldo, o.col0, o.rows, wn, o.cols},
+    store_all<MODE, EPI, S, S / 2>(a, acc, Place{o.out_row, o.ldo, o.col0, o.rows, wn, o.cols},
                                       [&](int i) { return wm + 16 * i; }, lane);
 }
 
-template <int MODE, bool LINEAR, int T, int RING, int KS>
+template <int MODE, Epilogue EPI, int T, int RING, int KS>
 static hipError_t launch(const MatmulArgs& a, hipStream_t stream) {
     constexpr int kLds = KS * RING * 2 * T * kStepR * 2;
     static LdsDevices allowed;
     const hipError_t e = allow_lds(
-        reinterpret_cast<const void*>(&matmul_tile_kernel<MODE, LINEAR, T, RING, KS>), kLds, allowed);
+        reinterpret_cast<const void*>(&matmul_tile_kernel<MODE, EPI, T, RING, KS>), kLds, allowed);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((matmul_tile_kernel<MODE, LINEAR, T, RING, KS>), block_grid(matmul_blocks<MODE, T, T>(a)),
+    hipLaunchKernelGGL((matmul_tile_kernel<MODE, EPI, T, RING, KS>), block_grid(matmul_blocks<MODE, T, T>(a)),
                        dim3(64 * kWaves * KS), kLds, stream, a);
     return hipGetLastError();
 }
 
 template <int T, int RING, int KS>
-static hipError_t launch_tile(int mode, bool linear, const MatmulArgs& a, hipStream_t stream) {
-    if (mode == kDx) return launch<kDx, false, T, RING, KS>(a, stream);
-    if (mode == kDw) return launch<kDw, false, T, RING, KS>(a, stream);
-    return linear ? launch<kFwd, true, T, RING, KS>(a, stream) : launch<kFwd, false, T, RING, KS>(a, stream);
+static hipError_t launch_tile(int mode, Epilogue epilogue, const MatmulArgs& a, hipStream_t stream) {
+    return with_mode(mode, epilogue, [&](auto m, auto e) {
+        return launch<decltype(m)::value, decltype(e)::value, T, RING, KS>(a, stream);
+    });
 }
 
 // The kernel that matmul_rule.h picks.
-hipError_t launch_matmul(int mode, bool linear, const MatmulArgs& a, hipStream_t stream) {
+hipError_t launch_matmul(int mode, Epilogue epilogue, const MatmulArgs& a, hipStream_t stream) {
     switch (choose_matmul(MatmulSizes{mode, a.P, a.E, a.N, a.K})) {
-        case MatmulKernel::kStream: return launch_matmul_stream(linear, a, stream);
-        case MatmulKernel::kSplit32: return launch_matmul_split(mode, linear, a, stream);
-        case MatmulKernel::kTile64Parts: return launch_tile<64, 3, 3>(mode, linear, a, stream);
-        case MatmulKernel::kTile64: return launch_tile<64, 4, 1>(mode, linear, a, stream);
-        case MatmulKernel::kTile128Deep: return launch_tile<128, 4, 1>(mode, linear, a, stream);
-        case MatmulKernel::kTile128: return launch_tile<128, 2, 1>(mode, linear, a, stream);
-        case MatmulKernel::kTile256: return launch_matmul256(mode, linear, a, stream);
+        case MatmulKernel::kStream: return launch_matmul_stream(epilogue, a, stream);
+        case MatmulKernel::kSplit32: return launch_matmul_split(mode, epilogue, a, stream);
+        case MatmulKernel::kTile64Parts: return launch_tile<64, 3, 3>(mode, epilogue, a, stream);
+        case MatmulKernel::kTile64: return launch_tile<64, 4, 1>(mode, epilogue, a, stream);
+        case MatmulKernel::kTile128Deep: return launch_tile<128, 4, 1>(mode, epilogue, a, stream);
+        case MatmulKernel::kTile128: return launch_tile<128, 2, 1>(mode, epilogue, a, stream);
+        case MatmulKernel::kTile256: return launch_matmul256(mode, epilogue, a, stream);
     }
     return hipErrorInvalidValue;
 }

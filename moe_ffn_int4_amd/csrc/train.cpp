@@ -73,9 +73,9 @@ int check_product(int64_t P, int64_t E, int64_t N, int64_t K, const int32_t* off
     return check_ptr(offsets, "offsets", 4);
 }
 
-int run_product(int mode, bool linear, const moe::MatmulArgs& a, void* stream) {
+int run_product(int mode, moe::Epilogue epilogue, const moe::MatmulArgs& a, void* stream) {
     CHECK(moe::device_ok());
-    HIP_CHECK(moe::launch_matmul(mode, linear, a, static_cast<hipStream_t>(stream)), "matmul launch");
+    HIP_CHECK(moe::launch_matmul(mode, epilogue, a, static_cast<hipStream_t>(stream)), "matmul launch");
     return MOE_OK;
 }
 
@@ -105,7 +105,7 @@ int moe_grouped_matmul(const uint16_t* x, const uint16_t* w, const int32_t* offs
     a.K = K;
     a.out = y;
     a.out_fp32 = out_fp32 != 0;
-    return run_product(moe::kFwd, false, a, stream);
+    return run_product(moe::kFwd, moe::Epilogue::kPlain, a, stream);
 }
 
 int moe_grouped_matmul_dx(const uint16_t* dy, const uint16_t* w, const int32_t* offsets, int64_t P, int64_t E,
@@ -130,7 +130,7 @@ int moe_grouped_matmul_dx(const uint16_t* dy, const uint16_t* w, const int32_t* 
     a.K = K;
     a.out = dx;
     a.out_fp32 = out_fp32 != 0;
-    return run_product(moe::kDx, false, a, stream);
+    return run_product(moe::kDx, moe::Epilogue::kPlain, a, stream);
 }
 
 int moe_grouped_matmul_dw(const uint16_t* dy, const uint16_t* x, const int32_t* offsets, int64_t P, int64_t E,
@@ -157,7 +157,7 @@ int moe_grouped_matmul_dw(const uint16_t* dy, const uint16_t* x, const int32_t* 
     a.out = dw;
     a.out_fp32 = out_fp32 != 0;
     a.accumulate = accumulate != 0;
-    return run_product(moe::kDw, false, a, stream);
+    return run_product(moe::kDw, moe::Epilogue::kPlain, a, stream);
 }
 
 int moe_linear(const uint16_t* x, const uint16_t* w, const float* bias, int32_t act, const uint16_t* residual,
@@ -193,7 +193,87 @@ int moe_linear(const uint16_t* x, const uint16_t* w, const float* bias, int32_t 
     a.residual = residual;
     a.z = z;
     a.act = act;
-    return run_product(moe::kFwd, true, a, stream);
+    return run_product(moe::kFwd, moe::Epilogue::kLinear, a, stream);
+}
+
+// A gated block's weights: h outputs over d inputs, `twice` for both matrices in one.
+static int check_gated(int64_t P, int64_t E, int64_t h, int64_t d, const int32_t* offsets, bool twice) {
+    CHECK(check_width(h, "h"));
+    if (h > kMaxDim / 2) return fail(MOE_ERR_INVALID_ARG, "h = %lld exceeds %lld", (long long)h, (long long)kMaxDim / 2);
+    // the rows of a tile of both matrices are 32-bit byte offsets from its first
+    if (twice && (h + 256) * d > (1LL << 31))
+        return fail(MOE_ERR_INVALID_ARG, "h = %lld with d = %lld: (h + 256) d exceeds 2^31", (long long)h, (long long)d);
+    return check_product(P, E, twice ? 2 * h : h, d, offsets);
+}
+
+int moe_gated(const uint16_t* x, const uint16_t* w, const float* bias, const int32_t* offsets, int32_t act, int64_t P,
+              int64_t E, int64_t h, int64_t d, uint16_t* y, uint16_t* z, void* stream) {
+    moe::clear_error();
+    CHECK(check_width(d, "d"));
+    CHECK(check_gated(P, E, h, d, offsets, true));
+    CHECK(check_act(act));
+    if (bias && offsets) return fail(MOE_ERR_INVALID_ARG, "bias with offsets: a dense block alone has one");
+    if (P == 0) return MOE_OK;
+    CHECK(check_ptr(x, "x"));
+    CHECK(check_ptr(w, "w"));
+    if (bias) CHECK(check_ptr(bias, "bias"));
+    CHECK(check_ptr(y, "y"));
+    if (z) CHECK(check_ptr(z, "z"));
+    const Span out{y, P * h * 2, "y"}, pre{z, P * h * 4, "z"};
+    for (const Span& s : {Span{x, P * d * 2, "x"}, Span{w, E * h * d * 4, "w"}, Span{bias, h * 8, "bias"},
+                          Span{offsets, (E + 1) * 4, "offsets"}}) {
+        CHECK(check_apart(out, s));
+        CHECK(check_apart(pre, s));
+    }
+    CHECK(check_apart(out, pre));
+    moe::MatmulArgs a{};
+    a.a = x;
+    a.b = w;
+    a.offsets = offsets;
+    a.P = P;
+    a.E = static_cast<int>(E);
+    a.N = 2 * h;
+    a.K = d;
+    a.out = y;
+    a.bias = bias;
+    a.z = z;
+    a.act = act;
+    return run_product(moe::kFwd, moe::Epilogue::kGated, a, stream);
+}
+
+int moe_gated_dz(const uint16_t* dy, const uint16_t* w2, const uint16_t* z, const int32_t* offsets, int32_t act,
+                 int64_t P, int64_t E, int64_t h, int64_t d, uint16_t* dz, uint16_t* y, void* stream) {
+    moe::clear_error();
+    CHECK(check_width(d, "d"));
+    CHECK(check_gated(P, E, h, d, offsets, false));
+    CHECK(check_act(act));
+    if (P == 0) return MOE_OK;
+    CHECK(check_ptr(dy, "dy"));
+    CHECK(check_ptr(w2, "w2"));
+    CHECK(check_ptr(z, "z"));
+    CHECK(check_ptr(dz, "dz"));
+    if (y) CHECK(check_ptr(y, "y"));
+    const Span out{dz, P * h * 4, "dz"}, again{y, P * h * 2, "y"}, pre{z, P * h * 4, "z"};
+    for (const Span& s : {Span{dy, P * d * 2, "dy"}, Span{w2, E * h * d * 2, "w2"}, Span{offsets, (E + 1) * 4, "offsets"}}) {
+        CHECK(check_apart(out, s));
+        CHECK(check_apart(again, s));
+    }
+    CHECK(check_apart(out, pre, true));
+    CHECK(check_apart(again, pre));
+    CHECK(check_apart(out, again));
+    moe::MatmulArgs a{};
+    a.a = dy;
+    a.b = w2;
+    a.offsets = offsets;
+    a.P = P;
+    a.E = static_cast<int>(E);
+    a.N = d;
+    a.K = h;
+    a.out = dz;
+    a.gate_z = z;
+    a.gate_y = y;
+    a.act = act;
+    return run_product(moe::kDx, moe::Epilogue::kGatedDz, a, stream);
 }
 
 size_t moe_linear_dz_workspace_bytes(int64_t T, int64_t N) {

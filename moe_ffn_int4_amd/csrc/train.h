@@ -28,12 +28,24 @@ struct MatmulArgs {
     const uint16_t* residual;  // [P, N] or null
     uint16_t* z;             // [P, N] or null
     int act;                 // MOE_ACT_*
+    // kFwd of a gated block: b holds gate and up rows [E, 2h, K] and N = 2h; out = act(g) u [P, h], z = [g | u]
+    // kDx of a gated block, K = h: out = the gradient of [g | u], from gate_z = [g | u] [P, 2h]
+    const uint16_t* gate_z;
+    uint16_t* gate_y;        // act(g) u [P, h], or null
 };
 
-hipError_t launch_matmul256(int mode, bool linear, const MatmulArgs& a, hipStream_t stream);
-hipError_t launch_matmul_split(int mode, bool linear, const MatmulArgs& a, hipStream_t stream);
-hipError_t launch_matmul_stream(bool linear, const MatmulArgs& a, hipStream_t stream);
-hipError_t launch_matmul(int mode, bool linear, const MatmulArgs& a, hipStream_t stream);
+// What is done with the products before they are stored.
+enum class Epilogue {
+    kPlain,    // rounded, or added to the old values
+    kLinear,   // kFwd: bias, activation, residual
+    kGated,    // kFwd: activation and product of the two projections
+    kGatedDz,  // kDx: the gradient through them
+};
+
+hipError_t launch_matmul256(int mode, Epilogue epilogue, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_matmul_split(int mode, Epilogue epilogue, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_matmul_stream(Epilogue epilogue, const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_matmul(int mode, Epilogue epilogue, const MatmulArgs& a, hipStream_t stream);
 
 // A launch has fewer than 2^32 threads along x: more blocks than kGridX stand in rows of
 // that many, the last of which may have blocks past the end.
