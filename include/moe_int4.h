@@ -429,6 +429,25 @@ int moe_gated_dz(const uint16_t *dy, const uint16_t *w2, const uint16_t *z, cons
                  void *stream);
 
 /*
+ * Products with 4-bit weights: moe_grouped_matmul and moe_linear on weights that
+ * moe_quantize_int4_tiled (or moe_quantize_int4 and moe_tile_int4) has written, at any number of rows, of which one token is the
+ * fastest to serve.
+ *   moe_grouped_matmul_int4:  y[s] = x[s] (scale * code)_e^T       q [E] x tiled [N, K], scales alike
+ *   moe_linear_int4:          y = act(x (scale * code)^T + bias) + residual
+ * x [P, K] bf16, y [P, N] bf16 or fp32 with out_fp32; offsets, bias, act and residual as there.
+ * N a multiple of 16, K of 128, group_size 128, 64 or 32 (the one it was quantized with). Scales may be any
+ * finite numbers. Codes are exact in the products, sums fp32, each group's sum multiplied by its fp32
+ * scale: no weight is rounded. A group's sum is formed as that of x (code + 24) less 24 times that of x, so an
+ * infinite x gives NaN in its row, and |x| is to stay below 2^110.
+ */
+int moe_grouped_matmul_int4(const uint16_t *x, const uint8_t *q, const float *scales,
+                            const int32_t *offsets, int64_t P, int64_t E, int64_t N, int64_t K,
+                            int32_t group_size, void *y, int32_t out_fp32, void *stream);
+int moe_linear_int4(const uint16_t *x, const uint8_t *q, const float *scales, const float *bias,
+                    int32_t act, const uint16_t *residual, int64_t T, int64_t N, int64_t K,
+                    int32_t group_size, void *y, int32_t out_fp32, void *stream);
+
+/*
  * SwiGLU of rows that hold both up-projections side by side, z = [g | u] [rows, 2h]:
  * y = silu(g) * u [rows, h]; and its gradient dz = [dy u silu'(g) | dy silu(g)]
  * [rows, 2h], which may be the same buffer as z.

@@ -151,6 +151,10 @@ def lib() -> ctypes.CDLL:
         L.moe_linear_dz_workspace_bytes.restype = sz
         L.moe_linear_dz.argtypes = [P, P, i32, i64, i64, P, P, P, sz, P]
         L.moe_linear_dz.restype = ctypes.c_int
+        L.moe_grouped_matmul_int4.argtypes = [P, P, P, P, i64, i64, i64, i64, i32, P, i32, P]
+        L.moe_grouped_matmul_int4.restype = ctypes.c_int
+        L.moe_linear_int4.argtypes = [P, P, P, P, i32, P, i64, i64, i64, i32, P, i32, P]
+        L.moe_linear_int4.restype = ctypes.c_int
         L.moe_gated.argtypes = [P, P, P, P, i32, i64, i64, i64, i64, P, P, P]
         L.moe_gated.restype = ctypes.c_int
         L.moe_gated_dz.argtypes = [P, P, P, P, i32, i64, i64, i64, i64, P, P, P]
@@ -833,6 +837,63 @@ def linear_dw(dz: torch.Tensor, x: torch.Tensor, out: Optional[torch.Tensor] = N
     _run(lib().moe_grouped_matmul_dw, dz, dz.data_ptr(), x.data_ptr(), None, T, 1, N, K,
          dw.data_ptr(), dw.dtype == torch.float32, bool(accumulate))
     return dw
+
+
+def _int4_weights(q: torch.Tensor, scales: torch.Tensor, dims: int):
+    """(shape of the weights, group) of tiled codes [.., N, K/2] and scales [.., N, K/group]."""
+    _need(q, "q", torch.uint8)
+    _need(scales, "scales", torch.float32)
+    if q.dim() != dims or scales.dim() != dims or scales.shape[:-1] != q.shape[:-1]:
+        raise ValueError(f"q {tuple(q.shape)} and scales {tuple(scales.shape)} must be "
+                         f"{'[E, N, K/2] and [E, N, K/group]' if dims == 3 else '[N, K/2] and [N, K/group]'}")
+    K, per = q.shape[-1] * 2, scales.shape[-1]
+    if per == 0 or K % per or K // per not in GROUPS:
+        raise ValueError(f"{K} columns with {per} scales a row: not a supported group {GROUPS}")
+    return (*q.shape[:-1], K), K // per
+
+
+def grouped_matmul_int4(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor,
+                        out: Optional[torch.Tensor] = None,
+                        out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """``grouped_matmul`` with int4 weights: y[s] = x[s] (scale * code)[e]^T.
+
+    q uint8 [E, N, K/2] and scales fp32 [E, N, K/group] in the tiled order of ``quantize_int4(tiled=True)`` or
+    ``tile_int4`` (``Int4Experts`` holds its matrices so); N a multiple of 16, K of 128. The weights are
+    not rounded to bf16."""
+    _two_dim(x, "x")
+    (E, N, K), group = _int4_weights(q, scales, 3)
+    _need(offsets, "offsets", torch.int32, (E + 1,))
+    _same_device(x, q, scales, offsets)
+    P = x.shape[0]
+    if x.shape[1] != K:
+        raise ValueError(f"x has {x.shape[1]} columns, q {K}")
+    y = _output(out, "out", (P, N), out.dtype if out is not None else out_dtype, x)
+    _run(lib().moe_grouped_matmul_int4, x, x.data_ptr(), q.data_ptr(), scales.data_ptr(), offsets.data_ptr(), P, E,
+         N, K, group, y.data_ptr(), y.dtype == torch.float32)
+    return y
+
+
+def linear_int4(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                act: str = "none", residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """``linear`` with int4 weights: act(x (scale * code)^T + bias) + residual, from one token on.
+
+    q uint8 [N, K/2] and scales fp32 [N, K/group], tiled as for ``grouped_matmul_int4``; bias fp32 [N],
+    residual bf16 [T, N], which a bf16 ``out`` may be itself."""
+    _two_dim(x, "x")
+    (N, K), group = _int4_weights(q, scales, 2)
+    T = x.shape[0]
+    if x.shape[1] != K:
+        raise ValueError(f"x has {x.shape[1]} columns, q {K}")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (N,))
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (T, N))
+    _same_device(x, q, scales, bias, residual)
+    y = _output(out, "out", (T, N), out.dtype if out is not None else out_dtype, x)
+    _run(lib().moe_linear_int4, x, x.data_ptr(), q.data_ptr(), scales.data_ptr(), _ptr(bias), _act(act), _ptr(residual),
+         T, N, K, group, y.data_ptr(), y.dtype == torch.float32)
+    return y
 
 
 def _gated(x, w, bias, offsets, act, z, out, E, h2, d):

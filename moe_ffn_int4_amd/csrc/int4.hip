@@ -1,0 +1,282 @@
+// int4.hip -- products with 4-bit weights, y[s] = x[s] (scale * code)^T, from a single row to
+// tiles of 128 rows.
+//
+// The reduction runs in steps of 128, one tile column of the weights' tiled order: a strip of 16
+// features is 1 KB of codes and 64 S bytes of scales a step (S = 128 / group), both contiguous, and
+// goes straight from HBM to LDS, as do 256 bytes of each row of x. A ring of stages keeps the next
+// steps under way. KS parts of the reduction, each a group of waves with a ring of its own,
+// take every KS-th step and add their sums in order at the end: a product of few rows has few
+// blocks, and more of its weights are then on their way at once.
+//
+// Codes reach the matrix cores exactly, as the bf16 numbers 16 + u, u = code + 8, which are the bits of
+// 16 with the nibble at the top of the mantissa. A group's sum of x * (16 + u) starts from -24 sum x, which
+// one more matrix instruction against the constant -24 gives for each fragment of x, shared by all
+// strips of a wave; what is left is the sum of x * code, in fp32, which the group's fp32 scale multiplies into
+// the accumulator. So no weight is ever rounded. (128 + u, the nibble at the bottom, saves a shift for eight
+// codes, but the sums that cancel are then over 136 |x|.)
+//
+// A wave multiplies MT sub-tiles of 16 rows by NS strips. Weights come first in the instruction, so that a lane holds four
+// consecutive columns of one row, as in matmul.h, whose stores the larger tiles use.
+#include "int4.h"
+
+#include "matmul.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kDepth = 128;  // of a step
+constexpr int kBand = 8;
+
+// ROWS: of x in a tile (4, or 16 WM MT); waves of a part: WM x WN; KS parts; RING stages
+template <int ROWS_, int WM_, int MT_, int WN_, int NS_, int KS_, int RING_>
+struct Shape {
+    static constexpr int ROWS = ROWS_, WM = WM_, MT = MT_, WN = WN_, NS = NS_, KS = KS_, RING = RING_;
+    static constexpr int kStrips = WN * NS, COLS = 16 * kStrips;
+    static constexpr int kPart = WM * WN, kThreads = 64 * kPart * KS;
+    static constexpr int kMine = kStrips / kPart;                   // strips whose codes a wave requests
+    static constexpr int kRowsMine = ROWS / kPart;                  // rows of x
+    static constexpr int kLoadsX = kRowsMine > 4 ? kRowsMine / 4 : 1;
+    static constexpr int kLoads = kLoadsX + kMine + 1;              // a wave's, a step
+    static constexpr int kX = ROWS * kDepth * 2, kW = kStrips * 1024;
+    static constexpr int stage(int S) { return kX + kW + kStrips * 64 * S; }
+    static constexpr int kSumRow = COLS * 4 + 16;                   // bytes, of the parts' sums
+    static constexpr int lds(int S) {
+        const int ring = KS * RING * stage(S), sums = KS > 1 ? KS * 16 * WM * MT * kSumRow : 0;
+        return ring > sums ? ring : sums;
+    }
+    static_assert(kMine * kPart == kStrips && kRowsMine * kPart == ROWS && (kRowsMine <= 4 || kRowsMine % 4 == 0),
+                  "loads are dealt evenly");
+    static_assert(lds(4) <= 160 * 1024, "LDS");
+};
+
+// 8 codes -> bf16 pairs 16 + u in order. A nibble's top bit flipped is u's; it and the bits of 16 are one XOR.
+__device__ __forceinline__ bf16x8 offset_codes(uint32_t w) {
+    constexpr uint32_t kMask = 0x00780078u, kFlip = 0x41C041C0u;  // bf16 16.0 | 0x40, twice
+    const uint32_t even = w << 3, odd = w >> 1;  // code 2j, 2j + 1 in bits 3 .. 6 of byte j
+    u32x4 r;
+    r[0] = (__builtin_amdgcn_perm(odd, even, 0x0C040C00u) & kMask) ^ kFlip;
+    r[1] = (__builtin_amdgcn_perm(odd, even, 0x0C050C01u) & kMask) ^ kFlip;
+    r[2] = (__builtin_amdgcn_perm(odd, even, 0x0C060C02u) & kMask) ^ kFlip;
+    r[3] = (__builtin_amdgcn_perm(odd, even, 0x0C070C03u) & kMask) ^ kFlip;
+    return __builtin_bit_cast(bf16x8, r);
+}
+
+// at most `steps` of the youngest steps' requests (PER a wave each) left in flight
+template <int PER, int MOST>
+__device__ __forceinline__ void wait_steps(int steps) {
+    if constexpr (MOST == 0) {
+        wait_loads<0>();
+    } else {
+        if (steps >= MOST) wait_loads<PER * MOST>();
+        else wait_steps<PER, MOST - 1>(steps);
+    }
+}
+
+}  // namespace
+
+template <typename Sh, bool LINEAR, int S>
+__global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
+    constexpr int ROWS = Sh::ROWS, MT = Sh::MT, NS = Sh::NS, KS = Sh::KS, RING = Sh::RING;
+    constexpr int kStage = Sh::stage(S);
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const MatmulArgs& a = args.m;
+    const int lane = threadIdx.x & 63;
+    const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = all_waves % Sh::kPart, part = all_waves / Sh::kPart;
+    MatTile t;
+    int rt, ct;
+    if (!find_tile<kFwd, ROWS, Sh::COLS, kBand>(a, lane, t, rt, ct)) return;
+
+    const int tiles = static_cast<int>(a.K) / kDepth;  // of a strip
+    const int strips = static_cast<int>(a.N / 16) - ct * Sh::kStrips;  // valid, from the tile's first
+    const int64_t strip0 = static_cast<int64_t>(t.group) * (a.N / 16) + static_cast<int64_t>(ct) * Sh::kStrips;
+    const uint8_t* q = reinterpret_cast<const uint8_t*>(
+        uniform(reinterpret_cast<uint64_t>(args.q + strip0 * tiles * 1024)));
+    const uint8_t* sc = reinterpret_cast<const uint8_t*>(
+        uniform(reinterpret_cast<uint64_t>(args.scales + strip0 * tiles * 16 * S)));
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(uniform(reinterpret_cast<uint64_t>(a.a + t.row0 * a.K)));
+
+    // this lane's sources at step 0, past the end the last valid ones: what they give is dropped
+    uint32_t off_x[Sh::kLoadsX];
+#pragma unroll
+    for (int i = 0; i < Sh::kLoadsX; ++i) {
+        const int r = wave * Sh::kRowsMine + 4 * i + (lane >> 4);
+        const int from = r < t.nrows ? r : t.nrows - 1;
+        // 16-byte pieces of a row XORed by the row, so that a fragment's 16 rows lie on different banks
+        off_x[i] = static_cast<uint32_t>(from * static_cast<int>(a.K) * 2 + (((lane & 15) ^ (r & 15)) * 16));
+    }
+    int64_t strip_q[Sh::kMine];  // uniform
+#pragma unroll
+    for (int i = 0; i < Sh::kMine; ++i) {
+        const int s = wave * Sh::kMine + i;
+        strip_q[i] = static_cast<int64_t>(s < strips ? s : strips - 1) * tiles * 1024;
+    }
+    const int s_strip = wave * Sh::kMine + lane / (4 * S);
+    const uint8_t* my_sc = sc + static_cast<int64_t>(s_strip < strips ? s_strip : strips - 1) * tiles * 64 * S +
+                           (lane % (4 * S)) * 16;
+    const int steps = (tiles - part + KS - 1) / KS, most = (tiles + KS - 1) / KS;  // this part's, and any's
+    const uint8_t* ring = lds + part * (RING * kStage);
+    const uint32_t ring_at = lds_address(ring);
+    auto request = [&](int stage, int k) __attribute__((always_inline)) {
+        const int g = part + k * KS;
+        const uint32_t at = ring_at + stage * kStage;
+#pragma unroll
+        for (int i = 0; i < Sh::kMine; ++i)
+            lds_load16(q + strip_q[i] + static_cast<int64_t>(g) * 1024, lane * 16,
+                       at + Sh::kX + (wave * Sh::kMine + i) * 1024);
+        if (lane < Sh::kMine * 4 * S)
+            lds_load16(my_sc + static_cast<int64_t>(g) * 64 * S, at + Sh::kX + Sh::kW + wave * Sh::kMine * 64 * S);
+        if (Sh::kRowsMine >= 4 || lane < 16 * Sh::kRowsMine) {
+#pragma unroll
+            for (int i = 0; i < Sh::kLoadsX; ++i)
+                lds_load16(x + g * (kDepth * 2), off_x[i], at + (wave * Sh::kRowsMine + 4 * i) * (kDepth * 2));
+        }
+    };
+    for (int k = 0; k < RING - 1 && k < steps; ++k) request(k, k);
+
+    const int i16 = lane & 15, qd = lane >> 4;
+    const int wm = wave / Sh::WN, wn = wave % Sh::WN;
+    const int xrow = wm * MT * 16 + (i16 < ROWS ? i16 : ROWS - 1);
+    const u32x4 minus = {0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};  // bf16 -24
+    f32x4 acc[MT][NS];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    int cur = 0, next = RING - 1;  // stages of step k and of step k + RING - 1
+    for (int k = 0; k < most; ++k) {
+        // step k has landed, and every wave has read step k - 1, whose stage is the next to be written
+        wait_steps<Sh::kLoads, RING - 2>(steps - 1 - k);
+        __syncthreads();
+        if (KS > 1 && k >= steps) break;  // the last round, of fewer parts
+        if (k + RING - 1 < steps) request(next, k + RING - 1);
+        const uint8_t* p = ring + cur * kStage;
+        const uint8_t* px = p + xrow * (kDepth * 2);
+        const uint8_t* pw = p + Sh::kX + wn * NS * 1024 + i16 * 16 + qd * 4;
+        const float* ps = reinterpret_cast<const float*>(p + Sh::kX + Sh::kW + wn * NS * 64 * S) + 4 * qd * S;
+        constexpr int PER = 4 / S;  // 32-deep slices of a group
+#pragma unroll
+        for (int g = 0; g < S; ++g) {
+            bf16x8 fx[PER][MT];
+#pragma unroll
+            for (int s = 0; s < PER; ++s)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    fx[s][i] = *reinterpret_cast<const bf16x8*>(px + i * 16 * (kDepth * 2) +
+                                                                (((4 * (g * PER + s) + qd) ^ (xrow & 15)) * 16));
+            f32x4 start[MT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                start[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < PER; ++s)
+                    start[i] = mfma_bf16(__builtin_bit_cast(bf16x8, minus), fx[s][i], start[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                f32x4 sum[MT];
+#pragma unroll
+                for (int s = 0; s < PER; ++s) {
+                    const bf16x8 fw =
+                        offset_codes(*reinterpret_cast<const uint32_t*>(pw + j * 1024 + (g * PER + s) * 256));
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) sum[i] = mfma_bf16(fw, fx[s][i], s == 0 ? start[i] : sum[i]);
+                }
+                f32x4 scale;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) scale[r] = ps[j * 16 * S + r * S + g];
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(scale[r], sum[i][r], acc[i][j][r]);
+            }
+        }
+        cur = cur == RING - 1 ? 0 : cur + 1;
+        next = next == RING - 1 ? 0 : next + 1;
+    }
+
+    const int cols = strips * 16 < Sh::COLS ? strips * 16 : Sh::COLS;
+    const int64_t col0 = static_cast<int64_t>(ct) * Sh::COLS;
+    if constexpr (KS > 1) {
+        // the parts' sums, in order, through LDS
+        constexpr int kSums = 16 * Sh::WM * MT * Sh::kSumRow;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+                *reinterpret_cast<f32x4*>(lds + part * kSums + ((wm * MT + i) * 16 + i16) * Sh::kSumRow +
+                                          ((wn * NS + j) * 16 + 4 * qd) * 4) = acc[i][j];
+        __syncthreads();
+        for (int e = threadIdx.x; e < t.nrows * (cols / 4); e += Sh::kThreads) {
+            const int r = e / (cols / 4), c = (e - r * (cols / 4)) * 4;
+            const uint8_t* from = lds + r * Sh::kSumRow + c * 4;
+            f32x4 v = *reinterpret_cast<const f32x4*>(from);
+#pragma unroll
+            for (int p = 1; p < KS; ++p) v += *reinterpret_cast<const f32x4*>(from + p * kSums);
+            const int64_t at = (t.row0 + r) * a.N + col0 + c;
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            if (LINEAR) {
+                if (a.bias) v += *reinterpret_cast<const f32x4*>(a.bias + col0 + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = act_value(v[i], a.act);
+                if (a.residual) {
+                    const u32x2 w = *reinterpret_cast<const u32x2*>(a.residual + at);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        v[2 * i] += __uint_as_float(w[i] << 16);
+                        v[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+                    }
+                }
+            }
+            if (a.out_fp32) *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = v;
+            else
+                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at) =
+                    u32x2{pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3])};
+        }
+    } else {
+        store_all<kFwd, LINEAR ? Epilogue::kLinear : Epilogue::kPlain, MT, NS / 2>(
+            a, acc, Place{t.row0, a.N, col0, t.nrows, wn * NS * 16, cols}, [&](int i) { return wm * MT * 16 + 16 * i; },
+            lane);
+    }
+}
+
+namespace {
+
+template <typename Sh, bool LINEAR, int S>
+hipError_t launch(const Int4Args& a, hipStream_t stream) {
+    static LdsDevices allowed;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(&int4_kernel<Sh, LINEAR, S>), Sh::lds(S), allowed);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((int4_kernel<Sh, LINEAR, S>), block_grid(matmul_blocks<kFwd, Sh::ROWS, Sh::COLS>(a.m)),
+                       dim3(Sh::kThreads), Sh::lds(S), stream, a);
+    return hipGetLastError();
+}
+
+template <typename Sh>
+hipError_t launch_shape(bool linear, int group, const Int4Args& a, hipStream_t stream) {
+    switch (group) {
+        case 128: return linear ? launch<Sh, true, 1>(a, stream) : launch<Sh, false, 1>(a, stream);
+        case 64: return linear ? launch<Sh, true, 2>(a, stream) : launch<Sh, false, 2>(a, stream);
+        default: return linear ? launch<Sh, true, 4>(a, stream) : launch<Sh, false, 4>(a, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_int4(Int4Shape shape, bool linear, int group, const Int4Args& a, hipStream_t stream) {
+    switch (shape) {
+        case Int4Shape::kFewWide: return launch_shape<Shape<4, 1, 1, 2, 1, 8, 5>>(linear, group, a, stream);
+        case Int4Shape::kFew: return launch_shape<Shape<4, 1, 1, 4, 1, 4, 3>>(linear, group, a, stream);
+        case Int4Shape::kRows16: return launch_shape<Shape<16, 1, 1, 4, 1, 4, 4>>(linear, group, a, stream);
+        case Int4Shape::kRows32: return launch_shape<Shape<32, 1, 2, 4, 1, 4, 3>>(linear, group, a, stream);
+        case Int4Shape::kRows64: return launch_shape<Shape<64, 1, 4, 4, 1, 2, 3>>(linear, group, a, stream);
+        case Int4Shape::kTile64: return launch_shape<Shape<64, 2, 2, 2, 4, 1, 3>>(linear, group, a, stream);
+        case Int4Shape::kTile128: return launch_shape<Shape<128, 2, 4, 4, 4, 1, 3>>(linear, group, a, stream);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace moe

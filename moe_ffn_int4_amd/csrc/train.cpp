@@ -10,6 +10,7 @@
 
 #include "adamw.h"
 #include "host.h"
+#include "int4.h"
 
 namespace {
 
@@ -194,6 +195,76 @@ int moe_linear(const uint16_t* x, const uint16_t* w, const float* bias, int32_t 
     a.z = z;
     a.act = act;
     return run_product(moe::kFwd, moe::Epilogue::kLinear, a, stream);
+}
+
+static int check_int4(int64_t P, int64_t E, int64_t N, int64_t K, int32_t group_size, const int32_t* offsets) {
+    if (group_size != 128 && group_size != 64 && group_size != 32)
+        return fail(MOE_ERR_INVALID_ARG, "group_size %d unsupported (128, 64 or 32)", group_size);
+    if (N < 16 || N % 16) return fail(MOE_ERR_INVALID_ARG, "N = %lld must be a positive multiple of 16", (long long)N);
+    if (K < 128 || K % 128)
+        return fail(MOE_ERR_INVALID_ARG, "K = %lld must be a positive multiple of 128", (long long)K);
+    CHECK(check_product(P, E, N, K, offsets));
+    // tiles of 4 rows are counted in 32 bits
+    if ((P / 4 + E) * (N / 32 + 1) > (1LL << 30))
+        return fail(MOE_ERR_INVALID_ARG, "P = %lld with E = %lld and N = %lld: too many tiles", (long long)P, (long long)E,
+                    (long long)N);
+    return MOE_OK;
+}
+
+static int run_int4(const uint16_t* x, const uint8_t* q, const float* scales, const int32_t* offsets, int64_t P, int64_t E,
+                    int64_t N, int64_t K, int32_t group_size, void* y, int32_t out_fp32, bool linear,
+                    moe::MatmulArgs& m, void* stream) {
+    CHECK(check_ptr(x, "x"));
+    CHECK(check_ptr(q, "q"));
+    CHECK(check_ptr(scales, "scales"));
+    CHECK(check_ptr(y, "y"));
+    const Span out{y, P * N * (out_fp32 ? 4 : 2), "y"};
+    CHECK(check_apart(out, {x, P * K * 2, "x"}));
+    CHECK(check_apart(out, {q, E * N * K / 2, "q"}));
+    CHECK(check_apart(out, {scales, E * N * (K / group_size) * 4, "scales"}));
+    CHECK(check_apart(out, {offsets, (E + 1) * 4, "offsets"}));
+    m.a = x;
+    m.offsets = offsets;
+    m.P = P;
+    m.E = static_cast<int>(E);
+    m.N = N;
+    m.K = K;
+    m.out = y;
+    m.out_fp32 = out_fp32 != 0;
+    CHECK(moe::device_ok());
+    HIP_CHECK(moe::launch_int4(moe::choose_int4(P, E, N), linear, group_size, moe::Int4Args{m, q, scales},
+                               static_cast<hipStream_t>(stream)),
+              "int4 product launch");
+    return MOE_OK;
+}
+
+int moe_grouped_matmul_int4(const uint16_t* x, const uint8_t* q, const float* scales, const int32_t* offsets, int64_t P,
+                            int64_t E, int64_t N, int64_t K, int32_t group_size, void* y, int32_t out_fp32,
+                            void* stream) {
+    moe::clear_error();
+    CHECK(check_int4(P, E, N, K, group_size, offsets));
+    if (P == 0) return MOE_OK;
+    moe::MatmulArgs m{};
+    return run_int4(x, q, scales, offsets, P, E, N, K, group_size, y, out_fp32, false, m, stream);
+}
+
+int moe_linear_int4(const uint16_t* x, const uint8_t* q, const float* scales, const float* bias, int32_t act,
+                    const uint16_t* residual, int64_t T, int64_t N, int64_t K, int32_t group_size, void* y,
+                    int32_t out_fp32, void* stream) {
+    moe::clear_error();
+    CHECK(check_int4(T, 1, N, K, group_size, nullptr));
+    CHECK(check_act(act));
+    if (T == 0) return MOE_OK;
+    if (bias) CHECK(check_ptr(bias, "bias"));
+    if (residual) CHECK(check_ptr(residual, "residual"));
+    const Span out{y, T * N * (out_fp32 ? 4 : 2), "y"};
+    CHECK(check_apart(out, {bias, N * 4, "bias"}));
+    CHECK(check_apart(out, {residual, T * N * 2, "residual"}, true));
+    moe::MatmulArgs m{};
+    m.bias = bias;
+    m.residual = residual;
+    m.act = act;
+    return run_int4(x, q, scales, nullptr, T, 1, N, K, group_size, y, out_fp32, true, m, stream);
 }
 
 // A gated block's weights: h outputs over d inputs, `twice` for both matrices in one.
