@@ -1,5 +1,5 @@
 // int4.hip -- products with 4-bit weights, y[s] = x[s] (scale * code)^T, from a single row to
-// tiles of 128 rows.
+// tiles of 64 rows.
 //
 // The reduction runs in steps of 128, one tile column of the weights' tiled order: a strip of 16
 // features is 1 KB of codes and 64 S bytes of scales a step (S = 128 / group), both contiguous, and
@@ -28,25 +28,26 @@ namespace {
 constexpr int kDepth = 128;  // of a step
 constexpr int kBand = 8;
 
-// ROWS: of x in a tile (4, or 16 WM MT); waves of a part: WM x WN; KS parts; RING stages
-template <int ROWS_, int WM_, int MT_, int WN_, int NS_, int KS_, int RING_>
+// ROWS of x in a tile; each of KS parts has WAVES waves, which take NS strips each; RING stages
+template <int ROWS_, int WAVES_, int NS_, int KS_, int RING_>
 struct Shape {
-    static constexpr int ROWS = ROWS_, WM = WM_, MT = MT_, WN = WN_, NS = NS_, KS = KS_, RING = RING_;
-    static constexpr int kStrips = WN * NS, COLS = 16 * kStrips;
-    static constexpr int kPart = WM * WN, kThreads = 64 * kPart * KS;
-    static constexpr int kMine = kStrips / kPart;                   // strips whose codes a wave requests
-    static constexpr int kRowsMine = ROWS / kPart;                  // rows of x
+    static constexpr int ROWS = ROWS_, WAVES = WAVES_, NS = NS_, KS = KS_, RING = RING_;
+    static constexpr int MT = (ROWS + 15) / 16;                     // sub-tiles of rows, all of them every wave's
+    static constexpr int kStrips = WAVES * NS, COLS = 16 * kStrips;
+    static constexpr int kThreads = 64 * WAVES * KS;
+    static constexpr int kRowsMine = ROWS / WAVES;                  // rows of x that a wave requests, beside its strips
     static constexpr int kLoadsX = kRowsMine > 4 ? kRowsMine / 4 : 1;
-    static constexpr int kLoads = kLoadsX + kMine + 1;              // a wave's, a step
+    static constexpr int kLoads = kLoadsX + NS + 1;                 // a wave's, a step
+    // sums meet in LDS before they are stored: of several parts, and of a single sub-tile, whose rows are not whole stores
+    static constexpr bool kJoin = KS > 1 || MT == 1;
     static constexpr int kX = ROWS * kDepth * 2, kW = kStrips * 1024;
     static constexpr int stage(int S) { return kX + kW + kStrips * 64 * S; }
     static constexpr int kSumRow = COLS * 4 + 16;                   // bytes, of the parts' sums
     static constexpr int lds(int S) {
-        const int ring = KS * RING * stage(S), sums = KS > 1 ? KS * 16 * WM * MT * kSumRow : 0;
+        const int ring = KS * RING * stage(S), sums = kJoin ? KS * 16 * MT * kSumRow : 0;
         return ring > sums ? ring : sums;
     }
-    static_assert(kMine * kPart == kStrips && kRowsMine * kPart == ROWS && (kRowsMine <= 4 || kRowsMine % 4 == 0),
-                  "loads are dealt evenly");
+    static_assert(kRowsMine * WAVES == ROWS && (kRowsMine <= 4 || kRowsMine % 4 == 0), "rows are dealt evenly");
     static_assert(lds(4) <= 160 * 1024, "LDS");
 };
 
@@ -83,7 +84,7 @@ __global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
     const MatmulArgs& a = args.m;
     const int lane = threadIdx.x & 63;
     const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wave = all_waves % Sh::kPart, part = all_waves / Sh::kPart;
+    const int wave = all_waves % Sh::WAVES, part = all_waves / Sh::WAVES;
     MatTile t;
     int rt, ct;
     if (!find_tile<kFwd, ROWS, Sh::COLS, kBand>(a, lane, t, rt, ct)) return;
@@ -106,27 +107,30 @@ __global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
         // 16-byte pieces of a row XORed by the row, so that a fragment's 16 rows lie on different banks
         off_x[i] = static_cast<uint32_t>(from * static_cast<int>(a.K) * 2 + (((lane & 15) ^ (r & 15)) * 16));
     }
-    int64_t strip_q[Sh::kMine];  // uniform
+    int64_t strip_q[NS];  // uniform
 #pragma unroll
-    for (int i = 0; i < Sh::kMine; ++i) {
-        const int s = wave * Sh::kMine + i;
+    for (int i = 0; i < NS; ++i) {
+        const int s = wave * NS + i;
         strip_q[i] = static_cast<int64_t>(s < strips ? s : strips - 1) * tiles * 1024;
     }
-    const int s_strip = wave * Sh::kMine + lane / (4 * S);
+    const int s_strip = wave * NS + lane / (4 * S);
     const uint8_t* my_sc = sc + static_cast<int64_t>(s_strip < strips ? s_strip : strips - 1) * tiles * 64 * S +
                            (lane % (4 * S)) * 16;
     const int steps = (tiles - part + KS - 1) / KS, most = (tiles + KS - 1) / KS;  // this part's, and any's
+    const int turn = ct % tiles;
     const uint8_t* ring = lds + part * (RING * kStage);
     const uint32_t ring_at = lds_address(ring);
     auto request = [&](int stage, int k) __attribute__((always_inline)) {
-        const int g = part + k * KS;
+        int g = part + k * KS;
+        if (KS == 1) g = g + turn < tiles ? g + turn : g + turn - tiles;
         const uint32_t at = ring_at + stage * kStage;
 #pragma unroll
-        for (int i = 0; i < Sh::kMine; ++i)
+        for (int i = 0; i < NS; ++i)
             lds_load16(q + strip_q[i] + static_cast<int64_t>(g) * 1024, lane * 16,
-                       at + Sh::kX + (wave * Sh::kMine + i) * 1024);
-        if (lane < Sh::kMine * 4 * S)
-            lds_load16(my_sc + static_cast<int64_t>(g) * 64 * S, at + Sh::kX + Sh::kW + wave * Sh::kMine * 64 * S);
+                       at + Sh::kX + (wave * NS + i) * 1024);
+        if (lane < NS * 4 * S)
+            lds_load16(my_sc + static_cast<int64_t>(g) * 64 * S,
+                       at + Sh::kX + Sh::kW + wave * NS * 64 * S);
         if (Sh::kRowsMine >= 4 || lane < 16 * Sh::kRowsMine) {
 #pragma unroll
             for (int i = 0; i < Sh::kLoadsX; ++i)
@@ -136,8 +140,7 @@ __global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
     for (int k = 0; k < RING - 1 && k < steps; ++k) request(k, k);
 
     const int i16 = lane & 15, qd = lane >> 4;
-    const int wm = wave / Sh::WN, wn = wave % Sh::WN;
-    const int xrow = wm * MT * 16 + (i16 < ROWS ? i16 : ROWS - 1);
+    const int xrow = i16 < ROWS ? i16 : ROWS - 1;
     const u32x4 minus = {0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};  // bf16 -24
     f32x4 acc[MT][NS];
 #pragma unroll
@@ -154,8 +157,8 @@ __global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
         if (k + RING - 1 < steps) request(next, k + RING - 1);
         const uint8_t* p = ring + cur * kStage;
         const uint8_t* px = p + xrow * (kDepth * 2);
-        const uint8_t* pw = p + Sh::kX + wn * NS * 1024 + i16 * 16 + qd * 4;
-        const float* ps = reinterpret_cast<const float*>(p + Sh::kX + Sh::kW + wn * NS * 64 * S) + 4 * qd * S;
+        const uint8_t* pw = p + Sh::kX + wave * NS * 1024 + i16 * 16 + qd * 4;
+        const float* ps = reinterpret_cast<const float*>(p + Sh::kX + Sh::kW + wave * NS * 64 * S) + 4 * qd * S;
         constexpr int PER = 4 / S;  // 32-deep slices of a group
 #pragma unroll
         for (int g = 0; g < S; ++g) {
@@ -196,19 +199,18 @@ __global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
         cur = cur == RING - 1 ? 0 : cur + 1;
         next = next == RING - 1 ? 0 : next + 1;
     }
-
     const int cols = strips * 16 < Sh::COLS ? strips * 16 : Sh::COLS;
     const int64_t col0 = static_cast<int64_t>(ct) * Sh::COLS;
-    if constexpr (KS > 1) {
+    if constexpr (Sh::kJoin) {
         // the parts' sums, in order, through LDS
-        constexpr int kSums = 16 * Sh::WM * MT * Sh::kSumRow;
+        constexpr int kSums = 16 * MT * Sh::kSumRow;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < NS; ++j)
-                *reinterpret_cast<f32x4*>(lds + part * kSums + ((wm * MT + i) * 16 + i16) * Sh::kSumRow +
-                                          ((wn * NS + j) * 16 + 4 * qd) * 4) = acc[i][j];
+                *reinterpret_cast<f32x4*>(lds + part * kSums + (i * 16 + i16) * Sh::kSumRow +
+                                          ((wave * NS + j) * 16 + 4 * qd) * 4) = acc[i][j];
         __syncthreads();
         for (int e = threadIdx.x; e < t.nrows * (cols / 4); e += Sh::kThreads) {
             const int r = e / (cols / 4), c = (e - r * (cols / 4)) * 4;
@@ -238,7 +240,7 @@ __global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
         }
     } else {
         store_all<kFwd, LINEAR ? Epilogue::kLinear : Epilogue::kPlain, MT, NS / 2>(
-            a, acc, Place{t.row0, a.N, col0, t.nrows, wn * NS * 16, cols}, [&](int i) { return wm * MT * 16 + 16 * i; },
+            a, acc, Place{t.row0, a.N, col0, t.nrows, wave * NS * 16, cols}, [&](int i) { return 16 * i; },
             lane);
     }
 }
@@ -255,6 +257,7 @@ hipError_t launch(const Int4Args& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// the shape is one of int4_rule.h, whose table has its sizes
 template <typename Sh>
 hipError_t launch_shape(bool linear, int group, const Int4Args& a, hipStream_t stream) {
     switch (group) {
@@ -268,13 +271,17 @@ hipError_t launch_shape(bool linear, int group, const Int4Args& a, hipStream_t s
 
 hipError_t launch_int4(Int4Shape shape, bool linear, int group, const Int4Args& a, hipStream_t stream) {
     switch (shape) {
-        case Int4Shape::kFewWide: return launch_shape<Shape<4, 1, 1, 2, 1, 8, 5>>(linear, group, a, stream);
-        case Int4Shape::kFew: return launch_shape<Shape<4, 1, 1, 4, 1, 4, 3>>(linear, group, a, stream);
-        case Int4Shape::kRows16: return launch_shape<Shape<16, 1, 1, 4, 1, 4, 4>>(linear, group, a, stream);
-        case Int4Shape::kRows32: return launch_shape<Shape<32, 1, 2, 4, 1, 4, 3>>(linear, group, a, stream);
-        case Int4Shape::kRows64: return launch_shape<Shape<64, 1, 4, 4, 1, 2, 3>>(linear, group, a, stream);
-        case Int4Shape::kTile64: return launch_shape<Shape<64, 2, 2, 2, 4, 1, 3>>(linear, group, a, stream);
-        case Int4Shape::kTile128: return launch_shape<Shape<128, 2, 4, 4, 4, 1, 3>>(linear, group, a, stream);
+        case Int4Shape::k4x16p8: return launch_shape<Shape<4, 1, 1, 8, 5>>(linear, group, a, stream);
+        case Int4Shape::k4x128p2: return launch_shape<Shape<4, 2, 4, 2, 2>>(linear, group, a, stream);
+        case Int4Shape::k16x32p8: return launch_shape<Shape<16, 1, 2, 8, 3>>(linear, group, a, stream);
+        case Int4Shape::k16x64p2: return launch_shape<Shape<16, 4, 1, 2, 4>>(linear, group, a, stream);
+        case Int4Shape::k16x256: return launch_shape<Shape<16, 4, 4, 1, 2>>(linear, group, a, stream);
+        case Int4Shape::k32x64p4: return launch_shape<Shape<32, 2, 2, 4, 2>>(linear, group, a, stream);
+        case Int4Shape::k32x128p2: return launch_shape<Shape<32, 4, 2, 2, 3>>(linear, group, a, stream);
+        case Int4Shape::k32x256: return launch_shape<Shape<32, 4, 4, 1, 2>>(linear, group, a, stream);
+        case Int4Shape::k64x128: return launch_shape<Shape<64, 4, 2, 1, 2>>(linear, group, a, stream);
+        case Int4Shape::k64x256: return launch_shape<Shape<64, 4, 4, 1, 2>>(linear, group, a, stream);
+        case Int4Shape::kCount: break;
     }
     return hipErrorInvalidValue;
 }

@@ -205,7 +205,7 @@ static int check_int4(int64_t P, int64_t E, int64_t N, int64_t K, int32_t group_
         return fail(MOE_ERR_INVALID_ARG, "K = %lld must be a positive multiple of 128", (long long)K);
     CHECK(check_product(P, E, N, K, offsets));
     // tiles of 4 rows are counted in 32 bits
-    if ((P / 4 + E) * (N / 32 + 1) > (1LL << 30))
+    if ((P / 4 + E) * (N / 16) > (1LL << 30))
         return fail(MOE_ERR_INVALID_ARG, "P = %lld with E = %lld and N = %lld: too many tiles", (long long)P, (long long)E,
                     (long long)N);
     return MOE_OK;
@@ -232,7 +232,7 @@ static int run_int4(const uint16_t* x, const uint8_t* q, const float* scales, co
     m.out = y;
     m.out_fp32 = out_fp32 != 0;
     CHECK(moe::device_ok());
-    HIP_CHECK(moe::launch_int4(moe::choose_int4(P, E, N), linear, group_size, moe::Int4Args{m, q, scales},
+    HIP_CHECK(moe::launch_int4(moe::choose_int4(P, E, N, K, group_size), linear, group_size, moe::Int4Args{m, q, scales},
                                static_cast<hipStream_t>(stream)),
               "int4 product launch");
     return MOE_OK;

@@ -75,10 +75,10 @@ def rule(tmp_path_factory):
 def test_the_cases_reach_every_shape(rule):
     lines, want = [], []
     for shape, counts, N, K in GROUPED:
-        lines.append(f"{sum(counts) + LEAD + TAIL} {len(counts)} {N}")
+        lines.append(f"{sum(counts) + LEAD + TAIL} {len(counts)} {N} {K} 128")
         want.append(shape)
     for shape, T, N, K in DENSE:
-        lines.append(f"{T} 1 {N}")
+        lines.append(f"{T} 1 {N} {K} 128")
         want.append(shape)
     got = subprocess.run([rule], input="\n".join(lines), capture_output=True, text=True, check=True).stdout.split()
     assert got == want
