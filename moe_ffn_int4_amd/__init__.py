@@ -25,6 +25,7 @@ untile_int4 / untile_scales / untile_bf16 convert them back to row-major.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from dataclasses import dataclass
@@ -1173,21 +1174,23 @@ def adamw(state: AdamWState, grads, step, lr, betas=(0.9, 0.999), eps: float = 1
     base_m, base_v, base_p = m.data_ptr(), v.data_ptr(), _ptr(state.master)
     width = 1 if bits == 8 else 4
     scale_m, scale_v = (_ptr(state.m_scale) or 0, _ptr(state.v_scale) or 0) if bits == 8 else (0, 0)
-    half = torch.bfloat16
-    for i, (p, g) in enumerate(zip(params, grads)):
-        if p.dtype not in _OUT or not p.is_contiguous() or p.get_device() != index or index < 0:
-            raise ValueError(f"parameter {i} must be bf16 or fp32, contiguous, and on the first one's GPU")
-        n, start = p.numel(), at
-        at += (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK * ADAMW_BLOCK
+    half, full, block = torch.bfloat16, torch.float32, ADAMW_BLOCK
+    add = words.extend
+    for p, g in zip(params, grads):
+        dtype, n, start = p.dtype, p.numel(), at
+        if (dtype is not half and dtype is not full) or not p.is_contiguous() or p.get_device() != index or index < 0:
+            raise ValueError("parameters must be bf16 or fp32, contiguous, and on one GPU")
+        at += -(-n // block) * block
         if g is None:
             continue
-        if g.dtype not in _OUT or not g.is_contiguous() or g.get_device() != index or g.shape != p.shape:
-            raise ValueError(f"gradient {i} must be bf16 or fp32, contiguous, of its parameter's shape and on its GPU")
-        p32, g32 = p.dtype is not half, g.dtype is not half
-        words += (p.data_ptr(), g.data_ptr(), 0 if p32 or base_p is None else base_p + 4 * start,
-                  base_m + width * start, base_v + width * start,
-                  scale_m and scale_m + start // ADAMW_BLOCK * 4, scale_v and scale_v + start // ADAMW_BLOCK * 4,
-                  n, int(p32) | int(g32) << 32)
+        gtype = g.dtype
+        if ((gtype is not half and gtype is not full) or not g.is_contiguous() or g.get_device() != index
+                or g.shape != p.shape):
+            raise ValueError("gradients must be bf16 or fp32, contiguous, of their parameter's shape and on its GPU")
+        add((p.data_ptr(), g.data_ptr(), base_p + 4 * start if base_p and dtype is half else 0,
+             base_m + width * start, base_v + width * start,
+             scale_m and scale_m + start // block * 4, scale_v and scale_v + start // block * 4,
+             n, (dtype is full) | (gtype is full) << 32))
     _need(m, "m", moment, (at,))
     _need(v, "v", moment, (at,))
     scales = (at // ADAMW_BLOCK,)
@@ -1211,8 +1214,8 @@ def adamw(state: AdamWState, grads, step, lr, betas=(0.9, 0.999), eps: float = 1
         h.grad_scale = _device_scalar(grad_scale, "grad_scale", torch.float32)
     _same_device(first, m, v, state.m_scale, state.v_scale, state.master, grad_scale,
                  step if isinstance(step, torch.Tensor) else None, lr if isinstance(lr, torch.Tensor) else None)
-    _run(lib().moe_adamw, first, (ctypes.c_uint64 * max(len(words), 1))(*words), len(words) // _ADAMW_WORDS,
-         ctypes.byref(h), bits)
+    table = array.array("Q", words)
+    _run(lib().moe_adamw, first, table.buffer_info()[0], len(words) // _ADAMW_WORDS, ctypes.byref(h), bits)
 
 
 def untile_int4(q: torch.Tensor, rows: int, K: int) -> torch.Tensor:
