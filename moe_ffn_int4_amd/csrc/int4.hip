@@ -275,6 +275,7 @@ hipError_t launch_int4(Int4Shape shape, bool linear, int group, const Int4Args& 
         case Int4Shape::k4x128p2: return launch_shape<Shape<4, 2, 4, 2, 2>>(linear, group, a, stream);
         case Int4Shape::k16x32p8: return launch_shape<Shape<16, 1, 2, 8, 3>>(linear, group, a, stream);
         case Int4Shape::k16x64p2: return launch_shape<Shape<16, 4, 1, 2, 4>>(linear, group, a, stream);
+        case Int4Shape::k16x64p4: return launch_shape<Shape<16, 2, 2, 4, 4>>(linear, group, a, stream);
         case Int4Shape::k16x256: return launch_shape<Shape<16, 4, 4, 1, 2>>(linear, group, a, stream);
         case Int4Shape::k32x64p4: return launch_shape<Shape<32, 2, 2, 4, 2>>(linear, group, a, stream);
         case Int4Shape::k32x128p2: return launch_shape<Shape<32, 4, 2, 2, 3>>(linear, group, a, stream);

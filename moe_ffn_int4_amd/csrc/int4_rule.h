@@ -14,6 +14,7 @@ enum class Int4Shape {
     k4x128p2,
     k16x32p8,
     k16x64p2,
+    k16x64p4,
     k16x256,
     k32x64p4,
     k32x128p2,
@@ -27,8 +28,8 @@ enum class Int4Shape {
 // for the steps of groups of 32, where n tiles fall on a CU and `steps` are the 128-deep
 // steps of one part. Fitted to 900 products of random sizes (1 to 8192 rows, 1 to 128 groups, N 64 to
 // 16384, K 128 to 8192) timed with 22 shapes; the times are met to 7 to 16 % (rms), and the shape of the
-// least estimate takes 3 % longer than the best of the 22 on average, 19 % and less in 95 of 100.
-// The ten were kept one by one for what each saves: with the first two alone 36 %.
+// least estimate takes 3 % longer than the best of the 22 on average, 15 % and less in 95 of 100.
+// The eleven were kept one by one for what each saves: with the best two alone 21 %.
 struct Int4Cost {
     int rows, cols, parts;
     double start, round, first, more, narrow;
@@ -42,6 +43,8 @@ constexpr Int4Cost kInt4Costs[] = {
     {16, 32, 8, 1.278, 2.391, 0.786, 0.945, 0.096},
     // 200 over E = 16, 8192 x 5120 91 (k32x64p4 121)
     {16, 64, 2, 2.247, 1.385, 0.458, 0.346, 0.137},
+    // 37 x 5120 x 8192, groups of 32: 17 (k32x64p4 21, k16x64p2 21)
+    {16, 64, 4, 1.036, 2.736, 0.754, 0.808, 0.112},
     {16, 256, 1, 2.582, 1.371, 0.725, 0.444, 0.340},
     // 64 x 5120 x 8192 18.9 (k16x64p2 27, k32x128p2 33, k64x128 54)
     {32, 64, 4, 0.860, 2.855, 0.956, 1.039, 0.112},
