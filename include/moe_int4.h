@@ -505,7 +505,7 @@ int moe_combine_backward(const uint16_t *dy, const void *o, int32_t o_fp32,
  * master, m, v and scales of every tensor) must not overlap itself or any gradient
  * (MOE_ERR_INVALID_ARG), so a tensor cannot be named twice. A NaN or infinite gradient leaves
  * that element's parameter and moments NaN or infinite (8 bits: an infinite one its whole block's
- * moments). Launches: one for each 52 tensors. No workspace; the tensors' addresses are copied
+ * moments); so does a number on the device below 1 to all. Launches: one for each 52 tensors. No workspace; the tensors' addresses are copied
  * at the call, so that a captured graph steps those tensors again.
  */
 #define MOE_ADAMW_BLOCK 128

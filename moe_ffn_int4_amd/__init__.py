@@ -15,7 +15,9 @@ functions below raises.
 
 The layer's steps are also there one by one with their gradients, on row-major bf16 weights:
 ``permute_rows``, ``grouped_matmul`` (``_dx``, ``_dw``), ``swiglu`` (``_backward``), ``combine``
-(``_backward``), and dense layers, ``linear`` (``linear_dz``, ``linear_dx``, ``linear_dw``).
+(``_backward``), and dense layers, ``linear`` (``linear_dz``, ``linear_dx``, ``linear_dw``). Gated blocks
+are one pass each way, ``grouped_gated`` and ``gated_linear`` (``_dz``), ``adamw`` steps many tensors at once, and
+``grouped_matmul_int4`` and ``linear_int4`` multiply by int4 weights outside the layer.
 They take no part in torch's autograd: results carry no graph, also where an argument requires
 gradients, and a program calls the gradients' functions itself (or in its own
 ``torch.autograd.Function``).
