@@ -430,8 +430,8 @@ int moe_gated_dz(const uint16_t *dy, const uint16_t *w2, const uint16_t *z, cons
 
 /*
  * Products with 4-bit weights: moe_grouped_matmul and moe_linear on weights that
- * moe_quantize_int4_tiled (or moe_quantize_int4 and moe_tile_int4) has written, at any number of rows, of which one token is the
- * fastest to serve.
+ * moe_quantize_int4_tiled (or moe_quantize_int4 and moe_tile_int4) has written, at any
+ * number of rows, from a single token on.
  *   moe_grouped_matmul_int4:  y[s] = x[s] (scale * code)_e^T       q [E] x tiled [N, K], scales alike
  *   moe_linear_int4:          y = act(x (scale * code)^T + bias) + residual
  * x [P, K] bf16, y [P, N] bf16 or fp32 with out_fp32; offsets, bias, act and residual as there.
@@ -505,8 +505,9 @@ int moe_combine_backward(const uint16_t *dy, const void *o, int32_t o_fp32,
  * master, m, v and scales of every tensor) must not overlap itself or any gradient
  * (MOE_ERR_INVALID_ARG), so a tensor cannot be named twice. A NaN or infinite gradient leaves
  * that element's parameter and moments NaN or infinite (8 bits: an infinite one its whole block's
- * moments); so does a number on the device below 1 to all. Launches: one for each 52 tensors. No workspace; the tensors' addresses are copied
- * at the call, so that a captured graph steps those tensors again.
+ * moments); so does a number on the device below 1 to all. Launches: one for each 52 tensors.
+ * No workspace; the tensors' addresses are copied at the call, so that a captured graph steps
+ * those tensors again.
  */
 #define MOE_ADAMW_BLOCK 128
 typedef struct moe_adamw_tensor {

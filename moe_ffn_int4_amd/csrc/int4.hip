@@ -160,6 +160,16 @@ __global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
         const uint8_t* pw = p + Sh::kX + wave * NS * 1024 + i16 * 16 + qd * 4;
         const float* ps = reinterpret_cast<const float*>(p + Sh::kX + Sh::kW + wave * NS * 64 * S) + 4 * qd * S;
         constexpr int PER = 4 / S;  // 32-deep slices of a group
+        // the scales of this lane's four features stand together, S each; where registers allow, all of them are
+        // read at once, 16 bytes at a time
+        constexpr bool AHEAD = NS * S <= 8;
+        f32x4 all[AHEAD ? NS * S : 1];
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+#pragma unroll
+                for (int v = 0; v < S; ++v) all[j * S + v] = *reinterpret_cast<const f32x4*>(ps + j * 16 * S + 4 * v);
+        }
 #pragma unroll
         for (int g = 0; g < S; ++g) {
             bf16x8 fx[PER][MT];
@@ -189,7 +199,8 @@ __global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
                 }
                 f32x4 scale;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) scale[r] = ps[j * 16 * S + r * S + g];
+                for (int r = 0; r < 4; ++r)
+                    scale[r] = AHEAD ? all[j * S + (r * S + g) / 4][(r * S + g) % 4] : ps[j * 16 * S + r * S + g];
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -275,11 +286,12 @@ hipError_t launch_int4(Int4Shape shape, bool linear, int group, const Int4Args& 
         case Int4Shape::k4x128p2: return launch_shape<Shape<4, 2, 4, 2, 2>>(linear, group, a, stream);
         case Int4Shape::k16x32p8: return launch_shape<Shape<16, 1, 2, 8, 3>>(linear, group, a, stream);
         case Int4Shape::k16x64p2: return launch_shape<Shape<16, 4, 1, 2, 4>>(linear, group, a, stream);
-        case Int4Shape::k16x64p4: return launch_shape<Shape<16, 2, 2, 4, 4>>(linear, group, a, stream);
+        case Int4Shape::k16x64p8: return launch_shape<Shape<16, 1, 4, 8, 2>>(linear, group, a, stream);
         case Int4Shape::k16x256: return launch_shape<Shape<16, 4, 4, 1, 2>>(linear, group, a, stream);
         case Int4Shape::k32x64p4: return launch_shape<Shape<32, 2, 2, 4, 2>>(linear, group, a, stream);
         case Int4Shape::k32x128p2: return launch_shape<Shape<32, 4, 2, 2, 3>>(linear, group, a, stream);
         case Int4Shape::k32x256: return launch_shape<Shape<32, 4, 4, 1, 2>>(linear, group, a, stream);
+        case Int4Shape::k48x64p4: return launch_shape<Shape<48, 2, 2, 4, 2>>(linear, group, a, stream);
         case Int4Shape::k64x128: return launch_shape<Shape<64, 4, 2, 1, 2>>(linear, group, a, stream);
         case Int4Shape::k64x256: return launch_shape<Shape<64, 4, 4, 1, 2>>(linear, group, a, stream);
         case Int4Shape::kCount: break;
