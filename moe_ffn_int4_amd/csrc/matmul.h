@@ -610,7 +610,9 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, const float* v) {
 
 // A gated block's outputs from sub-tiles that are gate and up by turns: each two give 16
 // columns of act(g) u. A pair of them (JJ = 2) goes out eight columns a lane, as above, a
-// single one four. z takes g and u as they were before the activation, rounded.
+// single one four. z takes g and u as they were before the activation, rounded. 8192 rows over 16
+// groups, h = 8192, d = 5120: 1201 us, with z 1245; the product of the same sizes takes 1217 and the
+// activation after it 68. A single row 29 us (5.8 TB/s).
 template <int ACT, int NI, int JJ, typename Row>
 __device__ __forceinline__ void store_gated(const MatmulArgs& a, const f32x4 (*acc)[2 * JJ], const Place& at,
                                             Row&& row0, int lane) {
@@ -664,7 +666,9 @@ __device__ __forceinline__ void store_gated(const MatmulArgs& a, const f32x4 (*a
 // The gradient of a gated block's projections, from that of its outputs (the products):
 // dz = [dh u act'(g) | dh act(g)], and act(g) u where it is wanted. g and u are loaded for two
 // sub-tile rows at once, ahead of the stores. Each place of dz is written by the lane
-// that read it of z, so that they may be one buffer.
+// that read it of z, so that they may be one buffer. At the sizes above 750 us, against 646 for
+// the product and 183 for the two passes after it: bound by the product, and then by the
+// 0.67 GB that all blocks move at once as their tiles end.
 template <int ACT, int NI, int JJ, typename Row>
 __device__ __forceinline__ void store_gated_dz(const MatmulArgs& a, const f32x4 (*acc)[2 * JJ], const Place& at,
                                                Row&& row0, int lane) {
