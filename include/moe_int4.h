@@ -498,12 +498,13 @@ int moe_combine_backward(const uint16_t *dy, const void *o, int32_t o_fp32,
  * ceil(n / 128) floats. The update takes the moments before they are rounded to codes. All
  * codes and scales 0 are a first step's moments. Rounding is to nearest: a decay of v by less
  * than half a step of its code (of up to 1/16 of sqrt(v)) is lost unless the block's largest
- * element decays with it, so beta2 near 1 forgets more slowly than in 32 bits.
+ * element decays with it, so beta2 near 1 forgets more slowly than in 32 bits; a sqrt(v) below
+ * 1/458752 of its block's largest is kept as 0, and eps alone then bounds that element's step if its gradient ends.
  *
  * Types may differ from tensor to tensor. n >= 0; together at most 2^34 elements. param and grad
  * are aligned to their type (16 bytes is faster), all else to 16 bytes. What is written (param,
- * master, m, v and scales of every tensor) must not overlap itself or any gradient
- * (MOE_ERR_INVALID_ARG), so a tensor cannot be named twice. A NaN or infinite gradient leaves
+ * master, m, v and scales of every tensor) must not overlap itself, any gradient or a number that
+ * the step reads from the device (MOE_ERR_INVALID_ARG), so a tensor cannot be named twice. A NaN or infinite gradient leaves
  * that element's parameter and moments NaN or infinite (8 bits: an infinite one its whole block's
  * moments); so does a number on the device below 1 to all. Launches: one for each 52 tensors.
  * No workspace; the tensors' addresses are copied at the call, so that a captured graph steps

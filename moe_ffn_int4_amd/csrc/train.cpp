@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdio>
 #include <memory>
 #include <new>
 
@@ -499,27 +500,32 @@ int moe_combine_backward(const uint16_t* dy, const void* o, int32_t o_fp32, cons
     return MOE_OK;
 }
 
-// What a step writes must be apart from itself and from every gradient: the spans sorted
-// by address, where each need only be apart from those that start before it ends.
-static int check_adamw_apart(const moe_adamw_tensor* tensors, int32_t count, int32_t bits) {
+// What a step writes must be apart from itself, from every gradient and from the numbers on the device: the
+// spans sorted by address, where each need only be apart from those that start before it ends.
+static int check_adamw_apart(const moe_adamw_tensor* tensors, int32_t count, const moe_adamw_hyper& hyper, int32_t bits) {
     struct Region {
         uintptr_t from, to;
-        const char* name;  // null: read alone
-        int32_t tensor;
+        const char* name;
+        int32_t tensor;  // or -1: of all
+        bool written;
     };
-    std::unique_ptr<Region[]> all(new (std::nothrow) Region[static_cast<size_t>(count) * 7]);
+    std::unique_ptr<Region[]> all(new (std::nothrow) Region[static_cast<size_t>(count) * 7 + 3]);
     if (!all) return fail(MOE_ERR_INVALID_ARG, "count = %d: no memory for its checks", count);
     size_t n = 0;
+    auto put = [&](const void* p, int64_t bytes, const char* name, int32_t tensor, bool written) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        if (p) all[n++] = Region{a, a + static_cast<uintptr_t>(bytes), name, tensor, written};
+    };
+    put(hyper.step_device, 4, "step_device", -1, false);
+    put(hyper.lr_device, 4, "lr_device", -1, false);
+    put(hyper.grad_scale, 4, "grad_scale", -1, false);
     for (int32_t i = 0; i < count; ++i) {
         const moe_adamw_tensor& t = tensors[i];
         if (t.n == 0) continue;
         const int64_t blocks = (t.n + MOE_ADAMW_BLOCK - 1) / MOE_ADAMW_BLOCK;
         const int64_t moment = bits == 8 ? blocks * MOE_ADAMW_BLOCK : t.n * 4;
-        auto add = [&](const void* p, int64_t bytes, const char* name) {
-            const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-            if (p) all[n++] = Region{a, a + static_cast<uintptr_t>(bytes), name, i};
-        };
-        add(t.grad, t.n * (t.grad_fp32 ? 4 : 2), nullptr);
+        auto add = [&](const void* p, int64_t bytes, const char* name) { put(p, bytes, name, i, true); };
+        put(t.grad, t.n * (t.grad_fp32 ? 4 : 2), "grad", i, false);
         add(t.param, t.n * (t.param_fp32 ? 4 : 2), "param");
         add(t.master, t.n * 4, "master");
         add(t.m, moment, "m");
@@ -534,11 +540,17 @@ static int check_adamw_apart(const moe_adamw_tensor* tensors, int32_t count, int
     for (size_t k = 0; k < n; ++k) {
         const Region& r = all[k];
         const Region* other = written && written->to > r.from ? written
-                              : r.name && read && read->to > r.from ? read : nullptr;
-        if (other)
-            return fail(MOE_ERR_INVALID_ARG, "%s of tensor %d overlaps %s of tensor %d", r.name ? r.name : "grad",
-                        r.tensor, other->name ? other->name : "grad", other->tensor);
-        const Region*& most = r.name ? written : read;
+                              : r.written && read && read->to > r.from ? read : nullptr;
+        if (other) {
+            char who[2][48];
+            for (int k = 0; k < 2; ++k) {
+                const Region& q = k ? *other : r;
+                if (q.tensor < 0) snprintf(who[k], sizeof who[k], "%s", q.name);
+                else snprintf(who[k], sizeof who[k], "%s of tensor %d", q.name, q.tensor);
+            }
+            return fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", who[0], who[1]);
+        }
+        const Region*& most = r.written ? written : read;
         if (!most || r.to > most->to) most = &r;
     }
     return MOE_OK;
@@ -587,7 +599,7 @@ int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, const moe_adamw_hy
         }
     }
     if (all == 0) return MOE_OK;
-    CHECK(check_adamw_apart(tensors, count, bits));
+    CHECK(check_adamw_apart(tensors, count, *hyper, bits));
     CHECK(moe::device_ok());
     HIP_CHECK(moe::launch_adamw(tensors, count, *hyper, bits, static_cast<hipStream_t>(stream)), "adamw launch");
     return MOE_OK;

@@ -131,3 +131,13 @@ def test_binding_refusals():
         moe.adamw(s, [], 1, 1e-3)
     with pytest.raises(ValueError):
         moe.adamw(s, [torch.zeros(8)], 1, 1e-3)  # not on a GPU
+
+
+@pytest.mark.parametrize("name", ["step_device", "lr_device", "grad_scale"])
+def test_numbers_that_the_step_would_overwrite(L, name):
+    for where in (at(0) + 1996, at(2) + 4, at(3), at(4) + 3996):
+        assert call(L, [tensor()], **{name: where}) == INVALID
+        assert name in said(L) and "of tensor 0" in said(L), said(L)
+    # a number may lie in a gradient, which is read alone, or right behind what is written
+    assert call(L, [tensor()], **{name: at(1)}) != INVALID
+    assert call(L, [tensor()], **{name: at(3) + 4000}) != INVALID
