@@ -57,6 +57,13 @@ struct Shape {
     static_assert(lds(4) <= 160 * 1024, "LDS");
 };
 
+// The order of a row's 16-byte pieces of x in LDS is XORed by this, so that the 16 lanes that are served
+// together, of 16 rows (half of them of the next quarter), touch different banks.
+template <int S>
+__device__ __forceinline__ int spread(int row) {
+    return S == 1 ? (row & 3) << 2 | (row >> 2 & 3) : row & 15;
+}
+
 // 8 codes -> bf16 pairs 16 + u in order. A nibble's top bit flipped is u's; it and the bits of 16 are one XOR.
 __device__ __forceinline__ bf16x8 offset_codes(uint32_t w) {
     constexpr uint32_t kMask = 0x00780078u, kFlip = 0x41C041C0u;  // bf16 16.0 | 0x40, twice
@@ -110,8 +117,7 @@ __global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
     for (int i = 0; i < Sh::kLoadsX; ++i) {
         const int r = wave * Sh::kRowsMine + 4 * i + (lane >> 4);
         const int from = r < t.nrows ? r : t.nrows - 1;
-        // 16-byte pieces of a row XORed by the row, so that a fragment's 16 rows lie on different banks
-        off_x[i] = static_cast<uint32_t>(from * static_cast<int>(a.K) * 2 + (((lane & 15) ^ (r & 15)) * 16));
+        off_x[i] = static_cast<uint32_t>(from * static_cast<int>(a.K) * 2 + (((lane & 15) ^ spread<S>(r)) * 16));
     }
     int64_t strip_q[NS];  // uniform
 #pragma unroll
@@ -163,7 +169,9 @@ __global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
         if (k + RING - 1 < steps) request(next, k + RING - 1);
         const uint8_t* p = ring + cur * kStage;
         const uint8_t* px = p + xrow * (kDepth * 2);
-        const uint8_t* pw = p + Sh::kX + wave * NS * 1024 + i16 * 16 + qd * 4;
+        // Which of a group's columns a lane's fragment has is free, as long as x and codes agree: with groups of 128 a lane
+        // takes its quarter's 32 codes in one read, with smaller ones eight of each slice
+        const uint8_t* pw = p + Sh::kX + wave * NS * 1024 + i16 * 16 + qd * (S == 1 ? 256 : 4);
         const float* ps = reinterpret_cast<const float*>(p + Sh::kX + Sh::kW + wave * NS * 64 * S) + 4 * qd * S;
         constexpr int PER = 4 / S;  // 32-deep slices of a group
         // the scales of this lane's four features stand together, S each; where registers allow, all of them are
@@ -184,7 +192,7 @@ __global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
                     fx[s][i] = *reinterpret_cast<const bf16x8*>(px + i * 16 * (kDepth * 2) +
-                                                                (((4 * (g * PER + s) + qd) ^ (xrow & 15)) * 16));
+                                                                (((S == 1 ? 4 * qd + s : 4 * (g * PER + s) + qd) ^ spread<S>(xrow)) * 16));
             f32x4 start[MT];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
@@ -196,10 +204,19 @@ __global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
                 f32x4 sum[MT];
+                uint32_t codes[PER];
+                if constexpr (S == 1) {
+                    const u32x4 all = *reinterpret_cast<const u32x4*>(pw + j * 1024);
+#pragma unroll
+                    for (int s = 0; s < PER; ++s) codes[s] = all[s];
+                } else {
+#pragma unroll
+                    for (int s = 0; s < PER; ++s)
+                        codes[s] = *reinterpret_cast<const uint32_t*>(pw + j * 1024 + (g * PER + s) * 256);
+                }
 #pragma unroll
                 for (int s = 0; s < PER; ++s) {
-                    const bf16x8 fw =
-                        offset_codes(*reinterpret_cast<const uint32_t*>(pw + j * 1024 + (g * PER + s) * 256));
+                    const bf16x8 fw = offset_codes(codes[s]);
 #pragma unroll
                     for (int i = 0; i < MT; ++i) sum[i] = mfma_bf16(fw, fx[s][i], s == 0 ? start[i] : sum[i]);
                 }
