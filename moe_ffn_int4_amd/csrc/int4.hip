@@ -67,12 +67,9 @@ __device__ __forceinline__ int spread(int row) {
 // 8 codes -> bf16 pairs 16 + u in order. A nibble's top bit flipped is u's; it and the bits of 16 are one XOR.
 __device__ __forceinline__ bf16x8 offset_codes(uint32_t w) {
     constexpr uint32_t kMask = 0x00780078u, kFlip = 0x41C041C0u;  // bf16 16.0 | 0x40, twice
-    const uint32_t even = w << 3, odd = w >> 1;  // code 2j, 2j + 1 in bits 3 .. 6 of byte j
     u32x4 r;
-    r[0] = (__builtin_amdgcn_perm(odd, even, 0x0C040C00u) & kMask) ^ kFlip;
-    r[1] = (__builtin_amdgcn_perm(odd, even, 0x0C050C01u) & kMask) ^ kFlip;
-    r[2] = (__builtin_amdgcn_perm(odd, even, 0x0C060C02u) & kMask) ^ kFlip;
-    r[3] = (__builtin_amdgcn_perm(odd, even, 0x0C070C03u) & kMask) ^ kFlip;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = (__umul24(w >> 8 * j & 0xFF, 0x8008) & kMask) ^ kFlip;  // b << 3 | b << 15
     return __builtin_bit_cast(bf16x8, r);
 }
 
@@ -90,7 +87,7 @@ __device__ __forceinline__ void wait_steps(int steps) {
 }  // namespace
 
 template <typename Sh, bool LINEAR, int S>
-__global__ __launch_bounds__(Sh::kThreads) void int4_kernel(Int4Args args) {
+__global__ __launch_bounds__(Sh::kThreads, 2) void int4_kernel(Int4Args args) {
     constexpr int ROWS = Sh::ROWS, MT = Sh::MT, NS = Sh::NS, KS = Sh::KS, RING = Sh::RING;
     constexpr int kStage = Sh::stage(S);
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
