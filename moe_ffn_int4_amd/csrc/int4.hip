@@ -53,6 +53,8 @@ struct Shape {
         const int ring = KS * RING * stage(S), sums = kJoin ? KS * 16 * MT * kSumRow : 0;
         return ring > sums ? ring : sums;
     }
+    // waves of a SIMD, as LDS allows: the compiler need not save registers for more
+    static constexpr int simd_waves(int S) { return 160 * 1024 / lds(S) * kThreads / 256; }
     static_assert(kRowsMine * WAVES == ROWS && (kRowsMine <= 4 || kRowsMine % 4 == 0), "rows are dealt evenly");
     static_assert(lds(4) <= 160 * 1024, "LDS");
 };
@@ -87,7 +89,7 @@ __device__ __forceinline__ void wait_steps(int steps) {
 }  // namespace
 
 template <typename Sh, bool LINEAR, int S>
-__global__ __launch_bounds__(Sh::kThreads, 2) void int4_kernel(Int4Args args) {
+__global__ __launch_bounds__(Sh::kThreads) __attribute__((amdgpu_waves_per_eu(2, Sh::simd_waves(S)))) void int4_kernel(Int4Args args) {
     constexpr int ROWS = Sh::ROWS, MT = Sh::MT, NS = Sh::NS, KS = Sh::KS, RING = Sh::RING;
     constexpr int kStage = Sh::stage(S);
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
