@@ -175,7 +175,7 @@ __global__ __launch_bounds__(Sh::kThreads) __attribute__((amdgpu_waves_per_eu(2,
         constexpr int PER = 4 / S;  // 32-deep slices of a group
         // the scales of this lane's four features stand together, S each; where registers allow, all of them are
         // read at once, 16 bytes at a time
-        constexpr bool AHEAD = NS * S <= 8;
+        constexpr bool AHEAD = NS * S <= (MT <= 2 ? 16 : 8);
         f32x4 all[AHEAD ? NS * S : 1];
         if constexpr (AHEAD) {
 #pragma unroll
