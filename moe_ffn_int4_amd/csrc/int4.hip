@@ -19,10 +19,10 @@
 // consecutive columns of one row, as in matmul.h, whose stores the larger tiles use.
 //
 // Steps of 128 are what one column of the tiled order has, so that every load is of a whole kilobyte. One row of
-// 8192 x 5120 takes 8 us (launch and one wait for HBM), 16 rows over 16 groups, 16384 x 5120, 88 us (5 TB/s, bound
-// by the requests to LDS: 86 without any arithmetic). Tens of rows are bound by the ten instructions of a widening, which a tile
-// of 16 rows repeats for each 16 (37 x 5120 x 8192 14 us); thousands by instruction issue, as products and other vector
-// instructions hardly overlap on a SIMD (4096 x 5120 x 8192 353 us, 970 TFLOP/s; groups of 64 409, of 32 535).
+// 8192 x 5120 takes 8 us (launch and one wait for HBM), 16 rows over 16 groups, 16384 x 5120, 79 to 93 us (5 to 5.8 TB/s, bound
+// by the requests to LDS). Tens of rows are bound by the eight instructions of a widening, which a tile of 16 rows repeats for each 16
+// (37 x 5120 x 8192 13.7 us); thousands by matrix instructions, a fifth of them the correction's, as these and other vector
+// instructions hardly overlap on a SIMD (4096 x 5120 x 8192 312 us, 1100 TFLOP/s; groups of 64 350, of 32 406).
 #include "int4.h"
 
 #include "matmul.h"
@@ -53,7 +53,8 @@ struct Shape {
         const int ring = KS * RING * stage(S), sums = kJoin ? KS * 16 * MT * kSumRow : 0;
         return ring > sums ? ring : sums;
     }
-    // waves of a SIMD, as LDS allows: the compiler need not save registers for more
+    // waves of a SIMD, as LDS allows: the compiler need not save registers for more (without this it reads a step's codes one
+    // by one, 100 x 5120 x 8192 24.0 us against 22.1); at least two, so that sums stay in ordinary registers
     static constexpr int simd_waves(int S) { return 160 * 1024 / lds(S) * kThreads / 256; }
     static_assert(kRowsMine * WAVES == ROWS && (kRowsMine <= 4 || kRowsMine % 4 == 0), "rows are dealt evenly");
     static_assert(lds(4) <= 160 * 1024, "LDS");
@@ -66,12 +67,13 @@ __device__ __forceinline__ int spread(int row) {
     return S == 1 ? (row & 3) << 2 | (row >> 2 & 3) : row & 15;
 }
 
-// 8 codes -> bf16 pairs 16 + u in order. A nibble's top bit flipped is u's; it and the bits of 16 are one XOR.
+// 8 codes -> bf16 pairs 16 + u in order. A byte times 2^3 + 2^15 has its nibbles at bits 3 and 19 (one instruction, which
+// picks the byte); a nibble's top bit flipped is u's, and it and the bits of 16 are one XOR (one more, with the mask).
 __device__ __forceinline__ bf16x8 offset_codes(uint32_t w) {
     constexpr uint32_t kMask = 0x00780078u, kFlip = 0x41C041C0u;  // bf16 16.0 | 0x40, twice
     u32x4 r;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = (__umul24(w >> 8 * j & 0xFF, 0x8008) & kMask) ^ kFlip;  // b << 3 | b << 15
+    for (int j = 0; j < 4; ++j) r[j] = (__umul24(w >> 8 * j & 0xFF, 0x8008) & kMask) ^ kFlip;
     return __builtin_bit_cast(bf16x8, r);
 }
 
@@ -89,7 +91,8 @@ __device__ __forceinline__ void wait_steps(int steps) {
 }  // namespace
 
 template <typename Sh, bool LINEAR, int S>
-__global__ __launch_bounds__(Sh::kThreads) __attribute__((amdgpu_waves_per_eu(2, Sh::simd_waves(S)))) void int4_kernel(Int4Args args) {
+__global__ __launch_bounds__(Sh::kThreads)
+__attribute__((amdgpu_waves_per_eu(2, Sh::simd_waves(S)))) void int4_kernel(Int4Args args) {
     constexpr int ROWS = Sh::ROWS, MT = Sh::MT, NS = Sh::NS, KS = Sh::KS, RING = Sh::RING;
     constexpr int kStage = Sh::stage(S);
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
@@ -311,9 +314,10 @@ hipError_t launch_int4(Int4Shape shape, bool linear, int group, const Int4Args& 
         case Int4Shape::k16x64p8: return launch_shape<Shape<16, 1, 4, 8, 2>>(linear, group, a, stream);
         case Int4Shape::k16x256: return launch_shape<Shape<16, 4, 4, 1, 2>>(linear, group, a, stream);
         case Int4Shape::k32x64p4: return launch_shape<Shape<32, 2, 2, 4, 2>>(linear, group, a, stream);
-        case Int4Shape::k32x128p2: return launch_shape<Shape<32, 4, 2, 2, 3>>(linear, group, a, stream);
+        case Int4Shape::k32x128p4: return launch_shape<Shape<32, 2, 4, 4, 2>>(linear, group, a, stream);
         case Int4Shape::k32x256: return launch_shape<Shape<32, 4, 4, 1, 2>>(linear, group, a, stream);
         case Int4Shape::k48x64p4: return launch_shape<Shape<48, 2, 2, 4, 2>>(linear, group, a, stream);
+        case Int4Shape::k48x256: return launch_shape<Shape<48, 4, 4, 1, 2>>(linear, group, a, stream);
         case Int4Shape::k64x128: return launch_shape<Shape<64, 4, 2, 1, 2>>(linear, group, a, stream);
         case Int4Shape::k64x256: return launch_shape<Shape<64, 4, 4, 1, 2>>(linear, group, a, stream);
         case Int4Shape::kCount: break;

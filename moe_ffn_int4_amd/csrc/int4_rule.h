@@ -17,9 +17,10 @@ enum class Int4Shape {
     k16x64p8,
     k16x256,
     k32x64p4,
-    k32x128p2,
+    k32x128p4,
     k32x256,
     k48x64p4,
+    k48x256,
     k64x128,
     k64x256,
     kCount,
@@ -29,37 +30,40 @@ enum class Int4Shape {
 // for the steps of groups of 32, where n tiles fall on a CU and `steps` are the 128-deep
 // steps of one part. Fitted to 1100 products of random sizes (1 to 8192 rows, 1 to 128 groups, N 64 to
 // 16384, K 128 to 8192) timed with 16 shapes; the times are met to 7 to 16 % (rms), and the shape of the
-// least estimate takes 2 % longer than the best of the 16 on average, 14 % and less in 95 of 100, 2.2 times
-// in the worst (few rows, dealt unevenly). The twelve were kept one by one for what each saves: of the best five alone
-// the least estimate takes 6 % longer.
+// least estimate takes 2.5 % longer than the best of the 16 on average, 17 % and less in 95 of 100, 1.7 times
+// in the worst (few rows, dealt unevenly). The thirteen were kept one by one for what each saves: of the best five alone
+// the least estimate takes 7 % longer.
 struct Int4Cost {
     int rows, cols, parts;
     double start, round, first, more, narrow;
 };
 constexpr Int4Cost kInt4Costs[] = {
-    // few strips: 1 x 1024 x 1024 3.6 us (k16x32p8 3.9, k16x64p2 4.6)
-    {4, 16, 8, 0.911, 2.640, 0.533, 0.579, 0.054},
-    // single rows of many experts: 16 over E = 16, 16384 x 5120 87 (k16x256 84, k16x64p2 103, k32x256 99)
-    {4, 128, 2, 3.049, 0.643, 0.717, 0.476, 0.337},
-    // few rows of one matrix: 1 x 8192 x 5120 7.7, 16 x 5120 x 8192 10.0 (k16x64p8 13.4, k16x64p2 15.8)
-    {16, 32, 8, 1.174, 2.457, 0.798, 0.936, 0.104},
-    // 200 over E = 16, 8192 x 5120 91 (k32x64p4 121)
-    {16, 64, 2, 2.282, 1.394, 0.474, 0.352, 0.062},
-    // 37 x 5120 x 8192 13.7 (k16x32p8 18.0, k32x64p4 18.3, k16x64p2 19.5)
-    {16, 64, 8, 1.354, 2.361, 1.249, 1.476, 0.124},
-    {16, 256, 1, 2.617, 1.373, 0.717, 0.438, 0.363},
-    // 64 x 5120 x 8192 18.9 (k16x64p2 27, k32x128p2 33, k64x128 54)
-    {32, 64, 4, 1.106, 2.769, 0.927, 1.046, 0.115},
-    // 128 x 5120 x 8192 32.4 (k32x64p4 36, k64x128 54)
-    {32, 128, 2, 0.852, 3.233, 0.873, 0.925, 0.150},
-    // 1000 over E = 16, 8192 x 5120 152 (k64x128 168, k64x256 157)
-    {32, 256, 1, 2.347, 1.209, 1.051, 0.667, 0.300},
-    // 100 x 5120 x 8192 25.5 (k32x128p2 32.6, k32x64p4 36.7)
-    {48, 64, 4, 0.970, 3.044, 1.183, 1.317, 0.228},
-    // 512 x 5120 x 8192 84 (k32x128p2 120, k64x256 89)
-    {64, 128, 1, 2.442, 1.083, 0.799, 0.534, 0.471},
-    // 4096 x 5120 x 8192 349 (k64x128 387; tiles of 128 x 256, one block a CU, 378)
-    {64, 256, 1, 2.248, 1.887, 1.257, 0.977, 0.611},
+    // few strips: 1 x 1024 x 1024 3.8 us (k16x32p8 4.4, k16x64p8 4.7)
+    {4, 16, 8, 0.761, 2.725, 0.514, 0.490, 0.090},
+    // single rows of many experts: 10 over E = 16, 5248 x 1664 11.6 (k16x256 14.0, k16x64p2 14.4)
+    {4, 128, 2, 2.955, 0.661, 0.629, 0.428, 0.297},
+    // few rows of one matrix: 1 x 8192 x 5120 7.5 (k16x64p8 9.5), 16 x 5120 x 8192 9.6 (k16x64p8 13.0, k32x64p4 17.3)
+    {16, 32, 8, 1.025, 2.484, 0.752, 0.826, 0.159},
+    // few rows of narrow experts: 110 over E = 64, 576 x 7552 27.9 (k32x128p4 31.7, k16x64p8 33.1)
+    {16, 64, 2, 2.116, 1.469, 0.444, 0.311, 0.101},
+    // 37 x 5120 x 8192 13.7 (k32x64p4 17.9, k16x32p8 18.4)
+    {16, 64, 8, 1.168, 2.468, 1.163, 1.326, 0.171},
+    // 16 over E = 16, 16384 x 5120 93 (k32x256 98, k16x64p2 118)
+    {16, 256, 1, 2.632, 1.341, 0.599, 0.394, 0.320},
+    // 64 x 5120 x 8192 17.9 (k48x64p4 22.6, k16x64p8 25.4)
+    {32, 64, 4, 0.903, 2.823, 0.836, 0.936, 0.231},
+    // 192 x 5120 x 8192 29.2 (k32x64p4 35.1, k48x64p4 43.3)
+    {32, 128, 4, 0.733, 3.357, 1.370, 1.485, 0.276},
+    // 1000 over E = 16, 8192 x 5120 131 (k48x256 139, k64x256 145)
+    {32, 256, 1, 2.315, 1.225, 0.799, 0.553, 0.259},
+    // 100 x 5120 x 8192 23.3 (k32x128p4 27.6, k32x64p4 33.9)
+    {48, 64, 4, 0.848, 3.100, 1.086, 1.166, 0.225},
+    // 500 over E = 16, 8192 x 5120 83 (k32x256 96, k64x256 98), 512 x 5120 x 8192 68 (k64x128 75)
+    {48, 256, 1, 1.943, 1.842, 0.974, 0.718, 0.262},
+    // thousands of rows, few columns: 3012 x 608 x 896 9.0 (k48x256 10.6, k64x256 11.9)
+    {64, 128, 1, 2.401, 1.031, 0.778, 0.505, 0.187},
+    // 4096 x 5120 x 8192 313 (k48x256 348, k64x128 352)
+    {64, 256, 1, 2.190, 1.887, 1.126, 0.894, 0.306},
 };
 static_assert(sizeof(kInt4Costs) / sizeof(Int4Cost) == static_cast<int>(Int4Shape::kCount), "a cost for each shape");
 
