@@ -493,17 +493,22 @@ int moe_combine_backward(const uint16_t *dy, const void *o, int32_t o_fp32,
  *
  * bits 32: m and v are fp32 [n]. bits 8: m and v hold OCP E4M3 codes of m and of sqrt(v) in
  * blocks of MOE_ADAMW_BLOCK elements with a scale each,
- *   most = max(max|x|, 2^-100),   scale = most / 448,   code = fp8_rne(x * (448 * (1 / most))),
+ *   most = max(max|x|, 2^-100),   scale = most / 448,   c = x * (448 * (1 / most)),   code = fp8_rne(c),
  * the last block filled up with zeros: m and v have ceil(n / 128) * 128 bytes, m_scale and v_scale
- * ceil(n / 128) floats. The update takes the moments before they are rounded to codes. All
- * codes and scales 0 are a first step's moments. Rounding is to nearest: a decay of v by less
- * than half a step of its code (of up to 1/16 of sqrt(v)) is lost unless the block's largest
- * element decays with it, so beta2 near 1 forgets more slowly than in 32 bits; a sqrt(v) below
- * 1/458752 of its block's largest is kept as 0, and eps alone then bounds that element's step if its gradient ends.
+ * ceil(n / 128) floats. What the codes leave is kept beside them, as many bytes again, `fine` bytes behind v:
+ * in the low four bits m's, in the high four sqrt(v)'s, a whole number k in [-7, 7],
+ *   k = floor((c - code) 14 / s + u),     x = (code + k s / 14) scale,
+ * with s the step between codes of code's exponent (2^-9 at least) and u in [0, 1) from a hash of the element's place in its
+ * tensor, the step's number and the new m. So a change of any size moves a moment by as much on
+ * average, where codes alone, whose step is 1/16 to 1/8 of them, would stay as they are for beta near 1 (v of beta2 = 0.99 for good
+ * after gradients fall or rise). The last digits are then random: sqrt(v) has a standard deviation of 1 % for beta2 = 0.95, 2 %
+ * for 0.99, 4 % for 0.999 and above (twice that while it falls to a tenth), m one of 0.6 % for beta1 = 0.9, 2 % for 0.99. The
+ * same call on the same state gives the same bits. The update takes the moments before they are rounded. All codes, scales and
+ * fine bytes 0 are a first step's moments; fine bytes 0 beside codes are those codes.
  *
  * Types may differ from tensor to tensor. n >= 0; together at most 2^34 elements. param and grad
  * are aligned to their type (16 bytes is faster), all else to 16 bytes. What is written (param,
- * master, m, v and scales of every tensor) must not overlap itself, any gradient or a number that
+ * master, m, v, fine bytes and scales of every tensor) must not overlap itself, any gradient or a number that
  * the step reads from the device (MOE_ERR_INVALID_ARG), so a tensor cannot be named twice. A NaN or infinite gradient leaves
  * that element's parameter and moments NaN or infinite (8 bits: an infinite one its whole block's
  * moments); so does a number on the device below 1 to all. Launches: one for each 52 tensors.
@@ -527,6 +532,7 @@ typedef struct moe_adamw_hyper {
     const int32_t *step_device; /* the number on the device, or NULL */
     const float *lr_device;     /* lr on the device (lr is then not read), or NULL */
     const float *grad_scale;    /* on the device, or NULL for 1 */
+    int64_t fine;               /* bits 8: bytes from each tensor's v to its fine bytes, a multiple of 16 but 0; else 0 */
 } moe_adamw_hyper;
 
 int moe_adamw(const moe_adamw_tensor *tensors, int32_t count, const moe_adamw_hyper *hyper,

@@ -79,7 +79,7 @@ class _AdamWHyper(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
                 ("step_device", ctypes.c_void_p), ("lr_device", ctypes.c_void_p),
-                ("grad_scale", ctypes.c_void_p)]
+                ("grad_scale", ctypes.c_void_p), ("fine", ctypes.c_int64)]
 
 
 _lib = None
@@ -1089,9 +1089,12 @@ class AdamWState:
 
     The moments of all parameters stand in one tensor each, parameter i's from ``starts()[i]``,
     a multiple of 128; what lies between them is zero and stays so. In 32 bits ``m`` and ``v`` are
-    fp32 [total]. In 8 bits they are uint8 [total], E4M3 codes of m and of sqrt(v), with fp32 scales
-    [total / 128]. ``master``, if there, holds the fp32 copies of bf16 parameters in the same places,
-    which a step updates and rounds to the parameters (what stands at an fp32 parameter's place is not used)."""
+    fp32 [total]. In 8 bits they are uint8, E4M3 codes of m and of sqrt(v), with fp32 scales
+    [total / 128]; ``m`` is [total], and ``v`` [2 total]: behind its codes stands a byte for each element with what both
+    moments' codes leave, four bits each (``fine``). A state may be made of codes alone, v [total]: its fine bytes
+    then start at 0, in a tensor of their own. ``master``, if there, holds the fp32 copies of bf16 parameters in the same
+    places as m, which a step updates and rounds to the parameters (what stands at an fp32 parameter's place is not used).
+    Of a state that is to go on elsewhere, keep all six, and ``fine`` where v is [total]."""
 
     params: list  # bf16 or fp32 tensors of any shape, contiguous, updated in place
     m: torch.Tensor
@@ -1100,9 +1103,21 @@ class AdamWState:
     v_scale: Optional[torch.Tensor] = None
     master: Optional[torch.Tensor] = None
 
+    def __post_init__(self):
+        self._fine = torch.zeros_like(self.v) if self.m.dtype == torch.uint8 and self.v.shape == self.m.shape else None
+
+    @property
+    def fine(self) -> Optional[torch.Tensor]:
+        """uint8 [total] with 8-bit moments: what their codes leave, m's in the low four bits, sqrt(v)'s in the high
+        four, in fourteenths of a code's step."""
+        if self.m.dtype != torch.uint8:
+            return None
+        total = self.m.numel()
+        return self.v[total:] if self.v.numel() == 2 * total else self._fine
+
     @staticmethod
     def zeros(params, bits: int = 32, master: bool = True) -> "AdamWState":
-        """State before the first step. ``bits``: of a moment, 32 or 8. ``master``: keep fp32
+        """State before the first step. ``bits``: of a moment, 32 or 8 (of its code; 12 with the fine bits). ``master``: keep fp32
         copies of bf16 parameters (without, a step smaller than half a bf16 step is lost)."""
         if bits not in (8, 32):
             raise ValueError(f"bits = {bits}: 8 or 32")
@@ -1111,7 +1126,7 @@ class AdamWState:
             raise ValueError("no parameters")
         total, dev = _adamw_starts(params)[-1], params[0].device
         moment = torch.uint8 if bits == 8 else torch.float32
-        m, v = (torch.zeros(total, dtype=moment, device=dev) for _ in range(2))
+        m, v = (torch.zeros(n, dtype=moment, device=dev) for n in (total, 2 * total if bits == 8 else total))
         scales = [torch.zeros(total // ADAMW_BLOCK, dtype=torch.float32, device=dev) if bits == 8 else None
                   for _ in range(2)]
         state = AdamWState(params, m, v, *scales)
@@ -1132,9 +1147,13 @@ class AdamWState:
         if self.m.dtype != torch.uint8:
             return tuple(t[at:at + n].reshape(p.shape).clone() for t in (self.m, self.v))
         end = self.starts()[i + 1]
-        out = []
-        for codes, scale in ((self.m, self.m_scale), (self.v, self.v_scale)):
-            x = codes[at:end].view(torch.float8_e4m3fn).float().reshape(-1, ADAMW_BLOCK)
+        out, fine = [], self.fine[at:end]
+        for codes, scale, k in ((self.m, self.m_scale, fine & 15), (self.v, self.v_scale, fine >> 4)):
+            x = codes[at:end].view(torch.float8_e4m3fn).float()
+            # 2^e of the code, its step times eight
+            power = (x.view(torch.int32) & 0x7F800000).clamp(min=0x3C800000).view(torch.float32)
+            k = torch.where(k > 7, k.float() - 16.0, k.float())
+            x = (x + k * (power * torch.tensor(1.0 / 112.0, device=x.device))).reshape(-1, ADAMW_BLOCK)
             x = x * scale[at // ADAMW_BLOCK:end // ADAMW_BLOCK].unsqueeze(1)
             out.append(x.reshape(-1)[:n].reshape(p.shape))
         return out[0], out[1] * out[1]
@@ -1194,7 +1213,10 @@ def adamw(state: AdamWState, grads, step, lr, betas=(0.9, 0.999), eps: float = 1
              scale_m and scale_m + start // block * 4, scale_v and scale_v + start // block * 4,
              n, (dtype is full) | (gtype is full) << 32))
     _need(m, "m", moment, (at,))
-    _need(v, "v", moment, (at,))
+    fine = state.fine if bits == 8 else None
+    _need(v, "v", moment, (2 * at,) if bits == 8 and v.numel() == 2 * at else (at,))
+    if bits == 8:
+        _need(fine, "fine", moment, (at,))
     scales = (at // ADAMW_BLOCK,)
     for t, name in ((state.m_scale, "m_scale"), (state.v_scale, "v_scale")):
         if bits == 8:
@@ -1214,7 +1236,9 @@ def adamw(state: AdamWState, grads, step, lr, betas=(0.9, 0.999), eps: float = 1
         h.lr = float(lr)
     if grad_scale is not None:
         h.grad_scale = _device_scalar(grad_scale, "grad_scale", torch.float32)
-    _same_device(first, m, v, state.m_scale, state.v_scale, state.master, grad_scale,
+    if fine is not None:
+        h.fine = fine.data_ptr() - base_v
+    _same_device(first, m, v, fine, state.m_scale, state.v_scale, state.master, grad_scale,
                  step if isinstance(step, torch.Tensor) else None, lr if isinstance(lr, torch.Tensor) else None)
     table = array.array("Q", words)
     _run(lib().moe_adamw, first, table.buffer_info()[0], len(words) // _ADAMW_WORDS, ctypes.byref(h), bits)

@@ -5,17 +5,26 @@
 // with p the 32-bit copy where there is one, else the parameter itself.
 //
 // Every element is read and written once: HBM bounds it, at 28 bytes an element for bf16
-// parameters and gradients with 32-bit copies and moments, at 16 with moments in 8 bits.
+// parameters and gradients with 32-bit copies and moments, at 18 with moments in 8 bits.
 // A block of 256 threads takes 2048 elements of one tensor, eight a thread, all its loads
-// (up to 112 bytes a thread) under way at once; a CU then has over 200 KB in flight. Loads are ordinary and stores
-// non-temporal: 120 M bf16 parameters with copies 620 us (5.4 TB/s; a 2 GiB copy runs at 5.05), with moments in 8 bits 339
-// (5.7). With non-temporal loads 645 and 344, with ordinary stores too 623 and 349; blocks of 1024 threads 624 and 343.
+// (up to 128 bytes a thread, 112 with bf16 gradients) under way at once; a CU's eight blocks then have over 200 KB in flight. Loads
+// are ordinary and stores non-temporal: 117 M bf16 parameters with copies 611 us (5.4 TB/s; a 2 GiB copy runs at 5.05), 118 M with
+// fp32 gradients and moments in 8 bits 432 (5.5). On another box, 120 M, moments in 8 bits without what is kept beside the codes: 620 and 339;
+// with non-temporal loads 645 and 344, with ordinary stores too 623 and 349; blocks of 1024 threads 624 and 343.
 //
 // Moments in 8 bits: m and sqrt(v) as E4M3 codes, 128 elements sharing a scale, most / 448 of
 // the block's largest magnitude (at least 2^-100). The root, not v: it halves the range of
 // exponents that a code has to cover (E4M3's 2^18 of the root are 2^36 of v), and the step
 // divides by it. The codes are rounded to nearest even; the update itself takes the moments
 // before that rounding. The 16 threads of a block of 128 find its maximum by DPP.
+//
+// A code's step is 6 to 12 % of it, and a step of the moments with beta changes them by 1 - beta of what they lack, so
+// codes alone stand still: sqrt(v) with beta2 = 0.999 stays 6 to 14 times too large where gradients fall to a tenth, 0.4 of its
+// value where they rise fourfold, and m with beta1 = 0.99 does not follow a change of sign. What rounding to a code leaves
+// is therefore kept beside it, in fourteenths of the code's step (-7 .. 7: the half step at both ends is one of the
+// values), four bits a moment, a byte an element for both. These are rounded up or down with the
+// probability of either's nearness, by a hash, so that their mean follows changes of any size: sqrt(v) over its value in 32
+// bits is 1.000 +- 0.016 (beta2 = 0.99) or 1.000 +- 0.036 (0.999) at rest, twice that while it falls to a tenth.
 //
 // Products and sums are rounded one by one, without fused multiply-adds: next to the border
 // between two codes the last bit of a moment decides which it becomes, and so the codes are
@@ -70,6 +79,7 @@ struct Args {
     const int32_t* step;
     double lr_host, log1, log2, decay;  // log of the betas
     int64_t step_host;
+    int64_t fine;  // bytes from v's codes to what is kept beside both moments'
 };
 static_assert(sizeof(Args) <= 4096, "a launch's arguments");
 
@@ -152,21 +162,50 @@ __device__ __forceinline__ float row_max(float v) {
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// eight codes and their block's scale
-__device__ __forceinline__ void decode8(u32x2 w, float scale, float (&x)[8]) {
+__device__ __forceinline__ void values8(u32x2 w, float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w[i]), false);
         const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w[i]), true);
-        x[4 * i] = a[0] * scale;
-        x[4 * i + 1] = a[1] * scale;
-        x[4 * i + 2] = b[0] * scale;
-        x[4 * i + 3] = b[1] * scale;
+        x[4 * i] = a[0];
+        x[4 * i + 1] = a[1];
+        x[4 * i + 2] = b[0];
+        x[4 * i + 3] = b[1];
     }
 }
 
-// the codes of a block of 128 (eight values a lane of a row); returns the scale
-__device__ __forceinline__ float encode8(const float (&x)[8], u32x2& w) {
+// 2^e of a code's value, its step times eight; subnormals have that of 2^-6
+__device__ __forceinline__ uint32_t code_power(float value) {
+    const uint32_t power = __float_as_uint(value) & 0x7F800000u;
+    return power > 0x3C800000u ? power : 0x3C800000u;
+}
+
+// eight codes, what is kept beside them (four bits of each byte from AT) and their block's scale
+template <int AT>
+__device__ __forceinline__ void decode8(u32x2 w, u32x2 fine, float scale, float (&x)[8]) {
+#pragma clang fp contract(off)
+    values8(w, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float n = static_cast<float>(static_cast<int32_t>(fine[i / 4] << (28 - 8 * (i % 4) - AT)) >> 28);
+        x[i] = (x[i] + n * (__uint_as_float(code_power(x[i])) * (1.0f / 112.0f))) * scale;
+    }
+}
+
+// Two 16-bit numbers for the roundings of element e's moments. The step's number is in `seed`; m's bits give others where that
+// stands still, as in a captured step that does not count.
+__device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t seed, float m) {
+    uint32_t x = (e * 0x9E3779B1u + seed) ^ __float_as_uint(m);
+    x = (x ^ x >> 15) * 0xD1B54A33u;
+    x = (x ^ x >> 13) * 0x8CB92BA7u;
+    return x ^ x >> 16;
+}
+
+// The codes of a block of 128 (eight values a lane of a row), and what they leave, in the four bits of each byte of `fine` that
+// start at AT (zeros before), as the same bits of `random` have it; returns the scale.
+template <int AT>
+__device__ __forceinline__ float encode8(const float (&x)[8], const uint32_t (&random)[8], u32x2& w, u32x2& fine) {
+#pragma clang fp contract(off)
     float most = 0x1p-100f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) most = fmaxf(most, __builtin_fabsf(x[i]));
@@ -183,6 +222,16 @@ __device__ __forceinline__ float encode8(const float (&x)[8], u32x2& w) {
     for (int i = 0; i < 2; ++i) {
         int k = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i], c[4 * i + 1], 0, false);
         w[i] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i + 2], c[4 * i + 3], k, true));
+    }
+    float value[8];
+    values8(w, value);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // 14 / step = 112 / power; 1 / power by its exponent
+        const float steps = (c[i] - value[i]) * (__uint_as_float(0x7F000000u - code_power(value[i])) * 112.0f);
+        const float up = static_cast<float>(random[i] >> (AT ? 16 : 0) & 0xFFFFu) * 0x1p-16f;
+        const int n = c[i] != c[i] ? 0 : static_cast<int>(floorf(steps + up));
+        fine[i / 4] |= static_cast<uint32_t>(n & 15) << (8 * (i % 4) + AT);
     }
     return most / 448.0f;
 }
@@ -228,8 +277,9 @@ __global__ __launch_bounds__(NT) void adamw_kernel(Args a) {
         } else {
             const u32x2 mc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(t.m) + e);
             const u32x2 vc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(t.v) + e);
-            decode8(mc, t.m_scale[block], m);
-            decode8(vc, t.v_scale[block], v);
+            const u32x2 fc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(t.v) + a.fine + e);
+            decode8<0>(mc, fc, t.m_scale[block], m);
+            decode8<4>(vc, fc, t.v_scale[block], v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = v[i] * v[i];
         }
@@ -258,11 +308,17 @@ __global__ __launch_bounds__(NT) void adamw_kernel(Args a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i >= left) m[i] = root[i] = 0.0f;
-        u32x2 mc, vc;
-        const float ms = encode8(m, mc), vs = encode8(root, vc);
+        const uint64_t number = DEVICE && a.step ? static_cast<uint64_t>(*a.step) : static_cast<uint64_t>(a.step_host);
+        const uint32_t seed = static_cast<uint32_t>(number) * 0xB5297A4Du + static_cast<uint32_t>(e >> 32) * 0x68E31DA5u;
+        uint32_t random[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) random[i] = dither(static_cast<uint32_t>(e) + i, seed, m[i]);
+        u32x2 mc, vc, fc = {0, 0};
+        const float ms = encode8<0>(m, random, mc, fc), vs = encode8<4>(root, random, vc, fc);
         if (base + (threadIdx.x & ~15u) * kEach < t.n) {
             __builtin_nontemporal_store(mc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(t.m) + e));
             __builtin_nontemporal_store(vc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(t.v) + e));
+            __builtin_nontemporal_store(fc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(t.v) + a.fine + e));
             if ((threadIdx.x & 15) == 0) {
                 t.m_scale[block] = ms;
                 t.v_scale[block] = vs;
@@ -288,6 +344,7 @@ hipError_t launch_adamw(const moe_adamw_tensor* tensors, int count, const moe_ad
     a.lr_host = h.lr;
     a.decay = h.weight_decay;
     a.step_host = h.step;
+    a.fine = h.fine;
     a.grad_scale = h.grad_scale;
     a.lr = h.lr_device;
     a.step = h.step_device;

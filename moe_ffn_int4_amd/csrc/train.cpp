@@ -509,7 +509,7 @@ static int check_adamw_apart(const moe_adamw_tensor* tensors, int32_t count, con
         int32_t tensor;  // or -1: of all
         bool written;
     };
-    std::unique_ptr<Region[]> all(new (std::nothrow) Region[static_cast<size_t>(count) * 7 + 3]);
+    std::unique_ptr<Region[]> all(new (std::nothrow) Region[static_cast<size_t>(count) * 8 + 3]);
     if (!all) return fail(MOE_ERR_INVALID_ARG, "count = %d: no memory for its checks", count);
     size_t n = 0;
     auto put = [&](const void* p, int64_t bytes, const char* name, int32_t tensor, bool written) {
@@ -533,6 +533,7 @@ static int check_adamw_apart(const moe_adamw_tensor* tensors, int32_t count, con
         if (bits == 8) {
             add(t.m_scale, blocks * 4, "m_scale");
             add(t.v_scale, blocks * 4, "v_scale");
+            if (hyper.fine) add(static_cast<const uint8_t*>(t.v) + hyper.fine, moment, "fine");
         }
     }
     std::sort(all.get(), all.get() + n, [](const Region& a, const Region& b) { return a.from < b.from; });
@@ -598,8 +599,12 @@ int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, const moe_adamw_hy
             return fail(MOE_ERR_INVALID_ARG, "m_scale and v_scale of tensor %d with bits 32", i);
         }
     }
+    if (hyper->fine && (bits == 32 || hyper->fine % 16))
+        return fail(MOE_ERR_INVALID_ARG, "fine = %lld: a multiple of 16 with bits 8, 0 with bits 32", (long long)hyper->fine);
     if (all == 0) return MOE_OK;
     CHECK(check_adamw_apart(tensors, count, *hyper, bits));
+    // codes alone lose every change of less than half their step: no state of bits 8 is without
+    if (bits == 8 && !hyper->fine) return fail(MOE_ERR_INVALID_ARG, "fine = 0 with bits 8");
     CHECK(moe::device_ok());
     HIP_CHECK(moe::launch_adamw(tensors, count, *hyper, bits, static_cast<hipStream_t>(stream)), "adamw launch");
     return MOE_OK;
