@@ -1180,8 +1180,9 @@ def adamw(state: AdamWState, grads, step, lr, betas=(0.9, 0.999), eps: float = 1
     ``grads``: a bf16 or fp32 tensor for each parameter, or None for one that is left alone.
     ``step``: this step's number, 1 for the first, and ``lr``: numbers, or tensors of one element
     on the GPU (int32, fp32), which a captured graph reads anew at each replay. ``grad_scale``
-    (fp32, one element on the GPU) multiplies the gradients: a clipping factor. Updates are
-    made behind torch's back: a parameter's version counter does not move."""
+    (fp32, one element on the GPU) multiplies the gradients: a clipping factor. As with torch's own
+    in-place operations a stepped parameter's version moves, so that a backward pass through a graph that still needs
+    its old values raises (a replayed graph of steps moves none)."""
     params, grads = state.params, list(grads)
     if len(grads) != len(params):
         raise ValueError(f"{len(grads)} gradients for {len(params)} parameters")
@@ -1191,7 +1192,7 @@ def adamw(state: AdamWState, grads, step, lr, betas=(0.9, 0.999), eps: float = 1
     moment = torch.uint8 if bits == 8 else torch.float32
     first = params[0]
     index = first.get_device()
-    words, at = [], 0
+    words, at, stepped = [], 0, []
     base_m, base_v, base_p = m.data_ptr(), v.data_ptr(), _ptr(state.master)
     width = 1 if bits == 8 else 4
     scale_m, scale_v = (_ptr(state.m_scale) or 0, _ptr(state.v_scale) or 0) if bits == 8 else (0, 0)
@@ -1208,6 +1209,7 @@ def adamw(state: AdamWState, grads, step, lr, betas=(0.9, 0.999), eps: float = 1
         if ((gtype is not half and gtype is not full) or not g.is_contiguous() or g.get_device() != index
                 or g.shape != p.shape):
             raise ValueError("gradients must be bf16 or fp32, contiguous, of their parameter's shape and on its GPU")
+        stepped.append(p)
         add((p.data_ptr(), g.data_ptr(), base_p + 4 * start if base_p and dtype is half else 0,
              base_m + width * start, base_v + width * start,
              scale_m and scale_m + start // block * 4, scale_v and scale_v + start // block * 4,
@@ -1242,6 +1244,7 @@ def adamw(state: AdamWState, grads, step, lr, betas=(0.9, 0.999), eps: float = 1
                  step if isinstance(step, torch.Tensor) else None, lr if isinstance(lr, torch.Tensor) else None)
     table = array.array("Q", words)
     _run(lib().moe_adamw, first, table.buffer_info()[0], len(words) // _ADAMW_WORDS, ctypes.byref(h), bits)
+    torch.autograd.graph.increment_version(stepped)
 
 
 def untile_int4(q: torch.Tensor, rows: int, K: int) -> torch.Tensor:
