@@ -882,7 +882,8 @@ def linear_int4(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, bias: Op
     """``linear`` with int4 weights: act(x (scale * code)^T + bias) + residual, from one token on.
 
     q uint8 [N, K/2] and scales fp32 [N, K/group], tiled as for ``grouped_matmul_int4``; bias fp32 [N],
-    residual bf16 [T, N], which a bf16 ``out`` may be itself."""
+    residual bf16 [T, N], which a bf16 ``out`` may be itself. Errors go by sum |x scale|, also under codes of 0 (up to 2^-17 of it):
+    below a bf16 result's rounding but for rows of a few very large x."""
     _two_dim(x, "x")
     (N, K), group = _int4_weights(q, scales, 2)
     T = x.shape[0]
