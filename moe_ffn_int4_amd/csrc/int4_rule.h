@@ -32,7 +32,11 @@ enum class Int4Shape {
 // 16384, K 128 to 8192) timed with 16 shapes; the times are met to 7 to 16 % (rms), and the shape of the
 // least estimate takes 2.5 % longer than the best of the 16 on average, 17 % and less in 95 of 100, 1.7 times
 // in the worst (few rows, dealt unevenly). The thirteen were kept one by one for what each saves: of the best five alone
-// the least estimate takes 7 % longer.
+// the least estimate takes 7 % longer. Beside each stands a product that it is chosen for, with its time and those of the next.
+//
+// Where it misses: a group's last tile counts as half empty, and tiles as if a CU had one at a time, so tens of rows an
+// expert can go to a neighbouring shape. By the least estimate 500 rows over 16 groups, 8192 x 5120, take tiles of 32 x 256, 89 us (of 48 x
+// 256 80); 1000 of 64 x 256, 145 (of 32 x 256 130); 110 over 64, 576 x 7552, of 16 x 64 in eight parts, 32 (in two parts 27).
 struct Int4Cost {
     int rows, cols, parts;
     double start, round, first, more, narrow;
@@ -44,7 +48,7 @@ constexpr Int4Cost kInt4Costs[] = {
     {4, 128, 2, 2.955, 0.661, 0.629, 0.428, 0.297},
     // few rows of one matrix: 1 x 8192 x 5120 7.5 (k16x64p8 9.5), 16 x 5120 x 8192 9.6 (k16x64p8 13.0, k32x64p4 17.3)
     {16, 32, 8, 1.025, 2.484, 0.752, 0.826, 0.159},
-    // few rows of narrow experts: 110 over E = 64, 576 x 7552 27.9 (k32x128p4 31.7, k16x64p8 33.1)
+    // tens of rows, short reductions: 59 x 2800 x 256 3.6 (k32x64p4 3.9, k16x64p8 4.1)
     {16, 64, 2, 2.116, 1.469, 0.444, 0.311, 0.101},
     // 37 x 5120 x 8192 13.7 (k32x64p4 17.9, k16x32p8 18.4)
     {16, 64, 8, 1.168, 2.468, 1.163, 1.326, 0.171},
@@ -54,11 +58,11 @@ constexpr Int4Cost kInt4Costs[] = {
     {32, 64, 4, 0.903, 2.823, 0.836, 0.936, 0.231},
     // 192 x 5120 x 8192 29.2 (k32x64p4 35.1, k48x64p4 43.3)
     {32, 128, 4, 0.733, 3.357, 1.370, 1.485, 0.276},
-    // 1000 over E = 16, 8192 x 5120 131 (k48x256 139, k64x256 145)
+    // 2867 over E = 128, 3200 x 1152 59 (k48x256 67, k16x256 76)
     {32, 256, 1, 2.315, 1.225, 0.799, 0.553, 0.259},
     // 100 x 5120 x 8192 23.3 (k32x128p4 27.6, k32x64p4 33.9)
     {48, 64, 4, 0.848, 3.100, 1.086, 1.166, 0.225},
-    // 500 over E = 16, 8192 x 5120 83 (k32x256 96, k64x256 98), 512 x 5120 x 8192 68 (k64x128 75)
+    // 1308 over E = 32, 8880 x 3840 142 (k32x256 174, k64x256 176), 512 x 5120 x 8192 66 (k64x128 73)
     {48, 256, 1, 1.943, 1.842, 0.974, 0.718, 0.262},
     // thousands of rows, few columns: 3012 x 608 x 896 9.0 (k48x256 10.6, k64x256 11.9)
     {64, 128, 1, 2.401, 1.031, 0.778, 0.505, 0.187},
