@@ -507,6 +507,10 @@ int moe_combine_backward(const uint16_t *dy, const void *o, int32_t o_fp32,
  * for 0.99, 4 % for 0.999 and above (twice that while it falls to a tenth), m one of 0.6 % for beta1 = 0.9, 2 % for 0.99. The
  * same call on the same state gives the same bits. The update takes the moments before they are rounded. All codes, scales and
  * fine bytes 0 are a first step's moments; fine bytes 0 beside codes are those codes.
+ * fine = 0: codes alone, for beta1 up to 0.9 and beta2 up to 0.95 (else MOE_ERR_INVALID_ARG). Changes of less than half a code's step
+ * are lost. With noisy gradients sqrt(v) of beta2 = 0.95 is within 0.8 and 1.5 of its value in 32 bits for 98 elements of 100, but
+ * follows a change more slowly (up to 2.5 times too large 60 steps after gradients fell to a tenth, in those bounds after 200);
+ * a gradient that is steady keeps m within 0.6 and 1.1 of its own, and sqrt(v) where it was as long as g^2 / v stays within 0 and 2.2.
  *
  * Types may differ from tensor to tensor. n >= 0; together at most 2^34 elements. param and grad
  * are aligned to their type (16 bytes is faster), all else to 16 bytes. What is written (param,
@@ -534,7 +538,7 @@ typedef struct moe_adamw_hyper {
     const int32_t *step_device; /* the number on the device, or NULL */
     const float *lr_device;     /* lr on the device (lr is then not read), or NULL */
     const float *grad_scale;    /* on the device, or NULL for 1 */
-    int64_t fine;               /* bits 8: bytes from each tensor's v to its fine bytes, a multiple of 16 but 0; else 0 */
+    int64_t fine;               /* bits 8: bytes from each tensor's v to its fine bytes, a multiple of 16, or 0; else 0 */
 } moe_adamw_hyper;
 
 int moe_adamw(const moe_adamw_tensor *tensors, int32_t count, const moe_adamw_hyper *hyper,

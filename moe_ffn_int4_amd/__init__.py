@@ -1092,10 +1092,10 @@ class AdamWState:
     a multiple of 128; what lies between them is zero and stays so. In 32 bits ``m`` and ``v`` are
     fp32 [total]. In 8 bits they are uint8, E4M3 codes of m and of sqrt(v), with fp32 scales
     [total / 128]; ``m`` is [total], and ``v`` [2 total]: behind its codes stands a byte for each element with what both
-    moments' codes leave, four bits each (``fine``). A state may be made of codes alone, v [total]: its fine bytes
-    then start at 0, in a tensor of their own. ``master``, if there, holds the fp32 copies of bf16 parameters in the same
-    places as m, which a step updates and rounds to the parameters (what stands at an fp32 parameter's place is not used).
-    Of a state that is to go on elsewhere, keep all six, and ``fine`` where v is [total]."""
+    moments' codes leave, four bits each (``fine``). A state may be made of codes alone, v [total], for betas up to 0.9 and
+    0.95: changes of less than half a code's step (3 to 6 %) are then lost, and slower moments would stand still. ``master``, if
+    there, holds the fp32 copies of bf16 parameters in the same places as m, which a step updates and rounds to the
+    parameters (what stands at an fp32 parameter's place is not used)."""
 
     params: list  # bf16 or fp32 tensors of any shape, contiguous, updated in place
     m: torch.Tensor
@@ -1104,17 +1104,12 @@ class AdamWState:
     v_scale: Optional[torch.Tensor] = None
     master: Optional[torch.Tensor] = None
 
-    def __post_init__(self):
-        self._fine = torch.zeros_like(self.v) if self.m.dtype == torch.uint8 and self.v.shape == self.m.shape else None
-
     @property
     def fine(self) -> Optional[torch.Tensor]:
-        """uint8 [total] with 8-bit moments: what their codes leave, m's in the low four bits, sqrt(v)'s in the high
-        four, in fourteenths of a code's step."""
-        if self.m.dtype != torch.uint8:
-            return None
+        """uint8 [total] behind the codes of an 8-bit v: what both moments' codes leave, m's in the low four bits, sqrt(v)'s in the
+        high four, in fourteenths of a code's step. None for codes alone and in 32 bits."""
         total = self.m.numel()
-        return self.v[total:] if self.v.numel() == 2 * total else self._fine
+        return self.v[total:] if self.m.dtype == torch.uint8 and self.v.numel() == 2 * total else None
 
     @staticmethod
     def zeros(params, bits: int = 32, master: bool = True) -> "AdamWState":
@@ -1148,13 +1143,15 @@ class AdamWState:
         if self.m.dtype != torch.uint8:
             return tuple(t[at:at + n].reshape(p.shape).clone() for t in (self.m, self.v))
         end = self.starts()[i + 1]
-        out, fine = [], self.fine[at:end]
-        for codes, scale, k in ((self.m, self.m_scale, fine & 15), (self.v, self.v_scale, fine >> 4)):
+        out, fine = [], self.fine
+        for codes, scale, shift in ((self.m, self.m_scale, 0), (self.v, self.v_scale, 4)):
             x = codes[at:end].view(torch.float8_e4m3fn).float()
-            # 2^e of the code, its step times eight
-            power = (x.view(torch.int32) & 0x7F800000).clamp(min=0x3C800000).view(torch.float32)
-            k = torch.where(k > 7, k.float() - 16.0, k.float())
-            x = (x + k * (power * torch.tensor(1.0 / 112.0, device=x.device))).reshape(-1, ADAMW_BLOCK)
+            if fine is not None:
+                # 2^e of the code, its step times eight
+                power = (x.view(torch.int32) & 0x7F800000).clamp(min=0x3C800000).view(torch.float32)
+                k = ((fine[at:end] >> shift) & 15).float()
+                x = x + torch.where(k > 7, k - 16.0, k) * (power * torch.tensor(1.0 / 112.0, device=x.device))
+            x = x.reshape(-1, ADAMW_BLOCK)
             x = x * scale[at // ADAMW_BLOCK:end // ADAMW_BLOCK].unsqueeze(1)
             out.append(x.reshape(-1)[:n].reshape(p.shape))
         return out[0], out[1] * out[1]
@@ -1217,9 +1214,7 @@ def adamw(state: AdamWState, grads, step, lr, betas=(0.9, 0.999), eps: float = 1
              n, (dtype is full) | (gtype is full) << 32))
     _need(m, "m", moment, (at,))
     fine = state.fine if bits == 8 else None
-    _need(v, "v", moment, (2 * at,) if bits == 8 and v.numel() == 2 * at else (at,))
-    if bits == 8:
-        _need(fine, "fine", moment, (at,))
+    _need(v, "v", moment, (at,) if fine is None else (2 * at,))
     scales = (at // ADAMW_BLOCK,)
     for t, name in ((state.m_scale, "m_scale"), (state.v_scale, "v_scale")):
         if bits == 8:
@@ -1241,7 +1236,7 @@ def adamw(state: AdamWState, grads, step, lr, betas=(0.9, 0.999), eps: float = 1
         h.grad_scale = _device_scalar(grad_scale, "grad_scale", torch.float32)
     if fine is not None:
         h.fine = fine.data_ptr() - base_v
-    _same_device(first, m, v, fine, state.m_scale, state.v_scale, state.master, grad_scale,
+    _same_device(first, m, v, state.m_scale, state.v_scale, state.master, grad_scale,
                  step if isinstance(step, torch.Tensor) else None, lr if isinstance(lr, torch.Tensor) else None)
     table = array.array("Q", words)
     _run(lib().moe_adamw, first, table.buffer_info()[0], len(words) // _ADAMW_WORDS, ctypes.byref(h), bits)

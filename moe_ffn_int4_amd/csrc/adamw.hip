@@ -5,11 +5,11 @@
 // with p the 32-bit copy where there is one, else the parameter itself.
 //
 // Every element is read and written once: HBM bounds it, at 28 bytes an element for bf16
-// parameters and gradients with 32-bit copies and moments, at 18 with moments in 8 bits.
+// parameters and gradients with 32-bit copies and moments, at 18 with moments in 8 bits (16 as codes alone).
 // A block of 256 threads takes 2048 elements of one tensor, eight a thread, all its loads
 // (up to 128 bytes a thread, 112 with bf16 gradients) under way at once; a CU's eight blocks then have over 200 KB in flight. Loads
 // are ordinary and stores non-temporal: 117 M bf16 parameters with copies 611 us (5.4 TB/s; a 2 GiB copy runs at 5.05), 118 M with
-// fp32 gradients and moments in 8 bits 432 (5.5). On another box, 120 M, moments in 8 bits without what is kept beside the codes: 620 and 339;
+// fp32 gradients and moments in 8 bits 427 (5.5), as codes alone 378 (5.6). On another box, 120 M, bf16 gradients, codes alone: 620 and 339;
 // with non-temporal loads 645 and 344, with ordinary stores too 623 and 349; blocks of 1024 threads 624 and 343.
 //
 // Moments in 8 bits: m and sqrt(v) as E4M3 codes, 128 elements sharing a scale, most / 448 of
@@ -24,7 +24,8 @@
 // is therefore kept beside it, in fourteenths of the code's step (-7 .. 7: the half step at both ends is one of the
 // values), four bits a moment, a byte an element for both. These are rounded up or down with the
 // probability of either's nearness, by a hash, so that their mean follows changes of any size: sqrt(v) over its value in 32
-// bits is 1.000 +- 0.016 (beta2 = 0.99) or 1.000 +- 0.036 (0.999) at rest, twice that while it falls to a tenth.
+// bits is 1.000 +- 0.016 (beta2 = 0.99) or 1.000 +- 0.036 (0.999) at rest, twice that while it falls to a tenth. Codes alone are taken
+// up to beta1 = 0.9 and beta2 = 0.95, where noise still carries them from code to code.
 //
 // Products and sums are rounded one by one, without fused multiply-adds: next to the border
 // between two codes the last bit of a moment decides which it becomes, and so the codes are
@@ -79,7 +80,7 @@ struct Args {
     const int32_t* step;
     double lr_host, log1, log2, decay;  // log of the betas
     int64_t step_host;
-    int64_t fine;  // bytes from v's codes to what is kept beside both moments'
+    int64_t fine;  // bytes from v's codes to what is kept beside both moments', or 0 for codes alone
 };
 static_assert(sizeof(Args) <= 4096, "a launch's arguments");
 
@@ -180,15 +181,18 @@ __device__ __forceinline__ uint32_t code_power(float value) {
     return power > 0x3C800000u ? power : 0x3C800000u;
 }
 
-// eight codes, what is kept beside them (four bits of each byte from AT) and their block's scale
-template <int AT>
+// eight codes, what is kept beside them (FINE: four bits of each byte from AT) and their block's scale
+template <bool FINE, int AT>
 __device__ __forceinline__ void decode8(u32x2 w, u32x2 fine, float scale, float (&x)[8]) {
 #pragma clang fp contract(off)
     values8(w, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float n = static_cast<float>(static_cast<int32_t>(fine[i / 4] << (28 - 8 * (i % 4) - AT)) >> 28);
-        x[i] = (x[i] + n * (__uint_as_float(code_power(x[i])) * (1.0f / 112.0f))) * scale;
+        if (FINE) {
+            const float n = static_cast<float>(static_cast<int32_t>(fine[i / 4] << (28 - 8 * (i % 4) - AT)) >> 28);
+            x[i] = x[i] + n * (__uint_as_float(code_power(x[i])) * (1.0f / 112.0f));
+        }
+        x[i] = x[i] * scale;
     }
 }
 
@@ -201,9 +205,9 @@ __device__ __forceinline__ uint32_t dither(uint32_t e, uint32_t seed, float m) {
     return x ^ x >> 16;
 }
 
-// The codes of a block of 128 (eight values a lane of a row), and what they leave, in the four bits of each byte of `fine` that
-// start at AT (zeros before), as the same bits of `random` have it; returns the scale.
-template <int AT>
+// The codes of a block of 128 (eight values a lane of a row), and with FINE what they leave, in the four bits of each byte of `fine`
+// that start at AT (zeros before), rounded by 16 bits of `random`; returns the scale.
+template <bool FINE, int AT>
 __device__ __forceinline__ float encode8(const float (&x)[8], const uint32_t (&random)[8], u32x2& w, u32x2& fine) {
 #pragma clang fp contract(off)
     float most = 0x1p-100f;
@@ -223,6 +227,7 @@ __device__ __forceinline__ float encode8(const float (&x)[8], const uint32_t (&r
         int k = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i], c[4 * i + 1], 0, false);
         w[i] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i + 2], c[4 * i + 3], k, true));
     }
+    if (!FINE) return most / 448.0f;
     float value[8];
     values8(w, value);
 #pragma unroll
@@ -238,6 +243,7 @@ __device__ __forceinline__ float encode8(const float (&x)[8], const uint32_t (&r
 
 }  // namespace
 
+// BITS of a moment: 32; 12, a code and what it leaves; 8, a code alone
 template <int BITS, bool DEVICE>
 __global__ __launch_bounds__(NT) void adamw_kernel(Args a) {
 #pragma clang fp contract(off)
@@ -269,7 +275,8 @@ __global__ __launch_bounds__(NT) void adamw_kernel(Args a) {
     else if (t.flags & kParam32) load8(static_cast<const float*>(t.param) + e, wide, left, p);
     else load8(static_cast<const uint16_t*>(t.param) + e, wide, left, p);
     const int64_t block = e / kAdamwBlock;
-    if (BITS == 8) {
+    constexpr bool FINE = BITS == 12;
+    if (BITS < 32) {
         // codes of whole blocks are there, also past n
         if (base + (threadIdx.x & ~15u) * kEach >= t.n) {
 #pragma unroll
@@ -277,9 +284,10 @@ __global__ __launch_bounds__(NT) void adamw_kernel(Args a) {
         } else {
             const u32x2 mc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(t.m) + e);
             const u32x2 vc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(t.v) + e);
-            const u32x2 fc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(t.v) + a.fine + e);
-            decode8<0>(mc, fc, t.m_scale[block], m);
-            decode8<4>(vc, fc, t.v_scale[block], v);
+            u32x2 fc = {0, 0};
+            if (FINE) fc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(t.v) + a.fine + e);
+            decode8<FINE, 0>(mc, fc, t.m_scale[block], m);
+            decode8<FINE, 4>(vc, fc, t.v_scale[block], v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = v[i] * v[i];
         }
@@ -303,22 +311,24 @@ __global__ __launch_bounds__(NT) void adamw_kernel(Args a) {
     if (t.master) save8(t.master + e, true, left, p);
     if (t.flags & kParam32) save8(static_cast<float*>(t.param) + e, wide, left, p);
     else save8(static_cast<uint16_t*>(t.param) + e, wide, left, p);
-    if (BITS == 8) {
+    if (BITS < 32) {
         // past n the moments are those of zeros
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i >= left) m[i] = root[i] = 0.0f;
-        const uint64_t number = DEVICE && a.step ? static_cast<uint64_t>(*a.step) : static_cast<uint64_t>(a.step_host);
-        const uint32_t seed = static_cast<uint32_t>(number) * 0xB5297A4Du + static_cast<uint32_t>(e >> 32) * 0x68E31DA5u;
-        uint32_t random[8];
+        uint32_t random[8] = {};
+        if (FINE) {
+            const int64_t number = DEVICE && a.step ? *a.step : a.step_host;
+            const uint32_t seed = static_cast<uint32_t>(number) * 0xB5297A4Du + static_cast<uint32_t>(e >> 32) * 0x68E31DA5u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) random[i] = dither(static_cast<uint32_t>(e) + i, seed, m[i]);
+            for (int i = 0; i < 8; ++i) random[i] = dither(static_cast<uint32_t>(e) + i, seed, m[i]);
+        }
         u32x2 mc, vc, fc = {0, 0};
-        const float ms = encode8<0>(m, random, mc, fc), vs = encode8<4>(root, random, vc, fc);
+        const float ms = encode8<FINE, 0>(m, random, mc, fc), vs = encode8<FINE, 4>(root, random, vc, fc);
         if (base + (threadIdx.x & ~15u) * kEach < t.n) {
             __builtin_nontemporal_store(mc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(t.m) + e));
             __builtin_nontemporal_store(vc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(t.v) + e));
-            __builtin_nontemporal_store(fc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(t.v) + a.fine + e));
+            if (FINE) __builtin_nontemporal_store(fc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(t.v) + a.fine + e));
             if ((threadIdx.x & 15) == 0) {
                 t.m_scale[block] = ms;
                 t.v_scale[block] = vs;
@@ -368,7 +378,10 @@ hipError_t launch_adamw(const moe_adamw_tensor* tensors, int count, const moe_ad
         }
         if (a.count == 0) break;
         const dim3 grid(static_cast<unsigned>(blocks));
-        if (bits == 8) {
+        if (bits == 8 && a.fine) {
+            if (device) hipLaunchKernelGGL((adamw_kernel<12, true>), grid, dim3(NT), 0, stream, a);
+            else hipLaunchKernelGGL((adamw_kernel<12, false>), grid, dim3(NT), 0, stream, a);
+        } else if (bits == 8) {
             if (device) hipLaunchKernelGGL((adamw_kernel<8, true>), grid, dim3(NT), 0, stream, a);
             else hipLaunchKernelGGL((adamw_kernel<8, false>), grid, dim3(NT), 0, stream, a);
         } else {

@@ -603,8 +603,10 @@ int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, const moe_adamw_hy
         return fail(MOE_ERR_INVALID_ARG, "fine = %lld: a multiple of 16 with bits 8, 0 with bits 32", (long long)hyper->fine);
     if (all == 0) return MOE_OK;
     CHECK(check_adamw_apart(tensors, count, *hyper, bits));
-    // codes alone lose every change of less than half their step: no state of bits 8 is without
-    if (bits == 8 && !hyper->fine) return fail(MOE_ERR_INVALID_ARG, "fine = 0 with bits 8");
+    // codes alone lose every change of less than half their step: with slower moments they stand still
+    if (bits == 8 && !hyper->fine && (hyper->beta1 > 0.9 || hyper->beta2 > 0.95))
+        return fail(MOE_ERR_INVALID_ARG, "beta1 = %g, beta2 = %g: at most 0.9 and 0.95 for codes alone (fine = 0 with bits 8)",
+                    hyper->beta1, hyper->beta2);
     CHECK(moe::device_ok());
     HIP_CHECK(moe::launch_adamw(tensors, count, *hyper, bits, static_cast<hipStream_t>(stream)), "adamw launch");
     return MOE_OK;

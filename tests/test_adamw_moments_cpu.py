@@ -25,13 +25,13 @@ INVALID = 1
 BASE = 0x10000000000
 
 
-def follow_v(beta2, scene, keep, seed=1, n=4096):
-    """sqrt(v) in 8 bits over sqrt(v) in 64, of the elements whose gradients changed (`one`: of the others)."""
+def follow_v(beta2, scene, keep, after=2, seed=1, n=4096):
+    """sqrt(v) in 8 bits over sqrt(v) in 64, `after` times 3 / (1 - beta2) steps after a change, of the elements whose gradients changed (`one`: of the others)."""
     r = np.random.default_rng(seed)
     half, one = np.arange(n) % 2 == 0, np.arange(n) % BLOCK == 0
     s, v = Moments(n, keep), np.zeros(n)
     warm = int(3 / (1 - beta2))
-    for t in range(3 * warm):
+    for t in range((1 + after) * warm):
         late = t >= warm
         g = r.standard_normal(n)
         if scene == "fall" and late:
@@ -58,6 +58,14 @@ def test_second_moments_follow(beta2, scene):
 def test_codes_alone_do_not_follow():
     """What the fine bits are for: without them sqrt(v) stands still."""
     assert follow_v(0.99, "fall", False).mean() > 5 and follow_v(0.999, "rise", False).mean() < 0.6
+
+
+@pytest.mark.parametrize("scene", ["rest", "fall", "rise", "one"])
+def test_codes_alone_at_their_largest_betas(scene):
+    """What is documented of them at beta2 = 0.95, 240 steps after a change."""
+    ratio = follow_v(0.95, scene, False, 4)
+    low, high = np.percentile(ratio, [1, 99])
+    assert 0.8 <= low and high <= 1.5, (low, high)
 
 
 @pytest.mark.parametrize("beta1,bound", [(0.9, 0.010), (0.95, 0.014), (0.99, 0.032)])
@@ -132,8 +140,7 @@ def test_where_a_state_keeps_them():
     s = moe.AdamWState.zeros(p, 8)
     assert s.m.shape == (384,) and s.v.shape == (768,) and s.fine.shape == (384,) and s.fine.data_ptr() == s.v.data_ptr() + 384
     alone = moe.AdamWState(p, s.m, s.v[:384], s.m_scale, s.v_scale)
-    assert alone.fine.shape == (384,) and alone.fine.dtype == torch.uint8 and not alone.fine.any()
-    assert alone.fine.data_ptr() != s.fine.data_ptr() and alone.fine.data_ptr() == alone.fine.data_ptr()
+    assert alone.fine is None and [t.shape for t in alone.moments(0)] == [(130,), (130,)]
     wide = moe.AdamWState.zeros(p, 32)
     assert wide.fine is None and wide.v.shape == (384,)
 
@@ -168,17 +175,17 @@ def at(i):
     return BASE + i * (1 << 44)
 
 
-def call(L, bits=8, fine=1 << 20, **kw):
+def call(L, bits=8, fine=1 << 20, betas=(0.9, 0.99), **kw):
     t = dict(param=at(0), grad=at(1), master=at(2), m=at(3), v=at(4), m_scale=at(5), v_scale=at(6), n=1000, types=0)
     t.update(kw)
     if bits == 32:
         t["m_scale"] = t["v_scale"] = 0
-    h = moe._AdamWHyper(1e-3, 0.9, 0.99, 1e-8, 0.1, 1, None, None, None, fine)
+    h = moe._AdamWHyper(1e-3, *betas, 1e-8, 0.1, 1, None, None, None, fine)
     return L.moe_adamw((ctypes.c_uint64 * 9)(*t.values()), 1, ctypes.byref(h), bits, None)
 
 
 @pytest.mark.parametrize("kw,needle", [
-    (dict(fine=0), "fine = 0 with bits 8"), (dict(fine=24), "fine = 24"), (dict(fine=-8), "fine = -8"), (dict(bits=32), "with bits 32"),
+    (dict(fine=0), "beta2 = 0.99"), (dict(fine=0, betas=(0.91, 0.95)), "beta1 = 0.91"), (dict(fine=0, betas=(0.0, 0.951)), "codes alone"), (dict(fine=24), "fine = 24"), (dict(fine=-8), "fine = -8"), (dict(bits=32), "with bits 32"),
     # over v's own codes, before and behind; over another buffer
     (dict(fine=1008), "overlaps"), (dict(fine=-1008), "overlaps"), (dict(fine=at(3) - at(4)), "overlaps"), (dict(fine=at(0) + 1984 - at(4)), "overlaps"),
     (dict(fine=at(1) - at(4) - 1008), "overlaps"),
@@ -193,4 +200,5 @@ def test_allowed(L):
     """Right behind or before the codes; the call then ends at the device, past the checks."""
     for fine in (1024, -1024, 1 << 20):
         assert call(L, fine=fine) != INVALID, L.moe_last_error()
-    assert call(L, bits=32, fine=0) != INVALID
+    assert call(L, bits=32, fine=0, betas=(0.99, 0.999)) != INVALID
+    assert call(L, fine=0, betas=(0.9, 0.95)) != INVALID

@@ -104,7 +104,8 @@ def test_a_captured_step_whose_number_stands_still():
 
 def _same(state, i, want, what):
     a, e = state.starts()[i], state.starts()[i + 1]
-    for got, ref, name in ((state.m[a:e], want.m, "m"), (state.v[a:e], want.v, "v"), (state.fine[a:e], want.fine, "fine"),
+    fine = torch.zeros(e - a) if state.fine is None else state.fine[a:e]
+    for got, ref, name in ((state.m[a:e], want.m, "m"), (state.v[a:e], want.v, "v"), (fine, want.fine, "fine"),
                            (state.m_scale[a // 128:e // 128], want.m_scale, "m_scale"), (state.v_scale[a // 128:e // 128], want.v_scale, "v_scale")):
         assert np.array_equal(got.cpu().numpy(), ref), f"{what}: {name}"
 
@@ -127,25 +128,31 @@ def test_codes_and_what_they_leave(betas, device):
     assert any(w.fine.any() for w in want) or betas[0] == 0.0
 
 
-def test_a_state_of_codes_alone():
-    """v [total]: fine bytes from 0, in a tensor of their own; a gradient that is None leaves them."""
+@pytest.mark.parametrize("alone", [False, True])
+def test_a_state_that_is_made_of_tensors(alone):
+    """With fine bytes behind v's codes, and of codes alone; a gradient that is None leaves all of it."""
     sizes = [300, 4000]
     r = np.random.default_rng(7)
-    plane = [torch.zeros(4480, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    plane = [torch.zeros(n, dtype=torch.uint8, device=DEV) for n in (4480, 4480 if alone else 8960)]
     state = moe.AdamWState([torch.zeros(n, device=DEV) for n in sizes], *plane, *(torch.zeros(35, device=DEV) for _ in range(2)))
-    want = [Moments(n) for n in sizes]
+    want = [Moments(n, not alone) for n in sizes]
     for t in range(4):
         grads = [r.standard_normal(n).astype(np.float32) for n in sizes]
-        kept = state.fine[:384].clone()
-        moe.adamw(state, [None if t == 2 else torch.from_numpy(grads[0]).to(DEV), torch.from_numpy(grads[1]).to(DEV)], t + 1, 1e-3)
+        moe.adamw(state, [None if t == 2 else torch.from_numpy(grads[0]).to(DEV), torch.from_numpy(grads[1]).to(DEV)], t + 1, 1e-3, betas=(0.9, 0.95))
         for i, (w, g) in enumerate(zip(want, grads)):
-            if i == 0 and t == 2:
-                assert torch.equal(state.fine[:384], kept)
-                continue
-            w.step(g, t + 1, (0.9, 0.999))
+            if i or t != 2:
+                w.step(g, t + 1, (0.9, 0.95))
             _same(state, i, w, f"step {t} tensor {i}")
-    with pytest.raises(ValueError):
-        moe.adamw(moe.AdamWState(state.params, state.m, state.v[:4096], state.m_scale, state.v_scale), [None, torch.zeros(4000, device=DEV)], 1, 1e-3)
+    zero = [None, torch.zeros(4000, device=DEV)]
+    for n in (4096, 0):
+        with pytest.raises(ValueError):
+            moe.adamw(moe.AdamWState(state.params, state.m, state.v[:n], state.m_scale, state.v_scale), zero, 1, 1e-3, betas=(0.9, 0.95))
+    if alone:
+        for betas in ((0.9, 0.999), (0.95, 0.95)):
+            with pytest.raises(moe.MoEError):
+                moe.adamw(state, zero, 1, 1e-3, betas=betas)
+        with pytest.raises(moe.MoEError):
+            moe.adamw(state, zero, 1, 1e-3)  # the default betas
 
 
 def test_past_32_bits():
