@@ -23,7 +23,8 @@
 // 8192 x 5120 takes 8 us (launch and one wait for HBM), 16 rows over 16 groups, 16384 x 5120, 79 to 93 us (5 to 5.8 TB/s, bound
 // by the requests to LDS). Tens of rows are bound by the eight instructions of a widening, which a tile of 16 rows repeats for each 16
 // (37 x 5120 x 8192 13.7 us); thousands by matrix instructions, a fifth of them the correction's, as these and other vector
-// instructions hardly overlap on a SIMD (4096 x 5120 x 8192 312 us, 1100 TFLOP/s; groups of 64 350, of 32 406).
+// instructions hardly overlap on a SIMD (4096 x 5120 x 8192 312 us, 1100 TFLOP/s; groups of 64 350, of 32 406;
+// 342 on the slowest of four boxes).
 #include "int4.h"
 
 #include "matmul.h"

@@ -666,7 +666,7 @@ __device__ __forceinline__ void store_gated(const MatmulArgs& a, const f32x4 (*a
 // The gradient of a gated block's projections, from that of its outputs (the products):
 // dz = [dh u act'(g) | dh act(g)], and act(g) u where it is wanted. g and u are loaded for two
 // sub-tile rows at once, ahead of the stores. Each place of dz is written by the lane
-// that read it of z, so that they may be one buffer. At the sizes above 750 us, against 646 for
+// that read it of z, so that they may be one buffer. At the sizes above 750 us (800 on the slowest of four boxes), against 646 for
 // the product and 183 for the two passes after it: bound by the product, and then by the
 // 0.67 GB that all blocks move at once as their tiles end.
 template <int ACT, int NI, int JJ, typename Row>
