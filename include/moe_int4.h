@@ -517,7 +517,8 @@ int moe_combine_backward(const uint16_t *dy, const void *o, int32_t o_fp32,
  * master, m, v, fine bytes and scales of every tensor) must not overlap itself, any gradient or a number that
  * the step reads from the device (MOE_ERR_INVALID_ARG), so a tensor cannot be named twice. A NaN or infinite gradient leaves
  * that element's parameter and moments NaN or infinite (8 bits: an infinite one its whole block's
- * moments); so does a number on the device below 1 to all. Launches: one for each 52 tensors.
+ * moments); so does a number on the device below 1 to all. A finite one whose square is not, past 1.8e19 after scaling, makes v
+ * infinite, so that its parameter stands still from then on (8 bits: its whole block's v). Launches: one for each 52 tensors.
  * No workspace; the tensors' addresses are copied at the call, so that a captured graph steps
  * those tensors again.
  */

@@ -155,6 +155,23 @@ def test_a_state_that_is_made_of_tensors(alone):
             moe.adamw(state, zero, 1, 1e-3)  # the default betas
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_gradient_whose_square_is_infinite(bits):
+    """v of its element (8 bits: of its block) is infinite, the step 0 but for the decay; other blocks and a clipped gradient are as ever."""
+    g = torch.ones(512, device=DEV)
+    g[130] = 1e20
+    for clip, hit in ((1.0, True), (1e-10, False)):
+        s = moe.AdamWState.zeros([torch.ones(512, device=DEV)], bits)
+        moe.adamw(s, [g], 1, 0.5, weight_decay=0.0, grad_scale=torch.tensor([clip], device=DEV))
+        p = s.params[0]
+        # a first step is lr g / (|g| + eps)
+        assert bool(torch.isfinite(p).all()) and abs(p[0].item() - (1 - 0.5 * clip / (clip + 1e-8))) <= 1e-6 and (p[130].item() == 1.0) == hit
+        m, v = s.moments(0)
+        bad = (~torch.isfinite(v)).nonzero().flatten().tolist()
+        assert bad == ([] if not hit else [130] if bits == 32 else list(range(128, 256))), bad
+        assert bool(torch.isfinite(m).all())
+
+
 def test_past_32_bits():
     """What the hash takes of an element's place past 2^32, and the fine bytes there."""
     n = (1 << 32) + 300
