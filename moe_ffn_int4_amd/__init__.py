@@ -1093,7 +1093,8 @@ class AdamWState:
     fp32 [total]. In 8 bits they are uint8, E4M3 codes of m and of sqrt(v), with fp32 scales
     [total / 128]; ``m`` is [total], and ``v`` [2 total]: behind its codes stands a byte for each element with what both
     moments' codes leave, four bits each (``fine``). A state may be made of codes alone, v [total], for betas up to 0.9 and
-    0.95: changes of less than half a code's step (3 to 6 %) are then lost, and slower moments would stand still. ``master``, if
+    0.95: changes of less than half a code's step (3 to 6 %) are then lost, and slower moments would stand still
+    (``torch.cat([v, torch.zeros_like(v)])`` makes of it one that keeps them). ``master``, if
     there, holds the fp32 copies of bf16 parameters in the same places as m, which a step updates and rounds to the
     parameters (what stands at an fp32 parameter's place is not used)."""
 

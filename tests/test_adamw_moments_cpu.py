@@ -141,6 +141,8 @@ def test_where_a_state_keeps_them():
     assert s.m.shape == (384,) and s.v.shape == (768,) and s.fine.shape == (384,) and s.fine.data_ptr() == s.v.data_ptr() + 384
     alone = moe.AdamWState(p, s.m, s.v[:384], s.m_scale, s.v_scale)
     assert alone.fine is None and [t.shape for t in alone.moments(0)] == [(130,), (130,)]
+    again = moe.AdamWState(p, s.m, torch.cat([alone.v, torch.zeros_like(alone.v)]), s.m_scale, s.v_scale)
+    assert not again.fine.any() and all(torch.equal(x, y) for i in (0, 1) for x, y in zip(again.moments(i), alone.moments(i)))
     wide = moe.AdamWState.zeros(p, 32)
     assert wide.fine is None and wide.v.shape == (384,)
 
